@@ -347,6 +347,76 @@ int lca_combine_shards(const float *parts, int n_shards, int B, const void *w_uv
 int lca_append_token(const void *rows, void *cache, int B, int64_t pitch, int64_t pos, const void *q,
                      void *ring, int g, int slot, void *q_dst, void *stream);
 
+/* ---- A cache in pages.  (Not part of the page's method: a server keeps the
+ * latent rows of sequences of changing length in pages of a common pool, and
+ * mixes single tokens and chunks of new tokens in one step.)
+ *
+ * pages [n_pages][page_size][576] bf16, page_size a power of two from 16 to
+ * 65536.  Row j of sequence b is row j % page_size of page
+ * block_table[b][j / page_size]; block_table is [B][max_blocks] int32.  An
+ * entry outside 0 .. n_pages-1 (such as -1) names no page.
+ *
+ * lca_page_tables: one step's bookkeeping on the device, in one launch.
+ * Sequence b holds ctx_lens[b] rows and gets new_lens[b] new ones (negative
+ * lengths count as 0, ctx_lens is clamped to max_blocks * page_size).  A new
+ * token that its row of the table (max_blocks * page_size rows) or the batch
+ * (max_tokens, in the order of the sequences) has no room for is dropped;
+ * with n_b the tokens kept:
+ *   q_start    [B+1] out: first new token of each sequence; q_start[B] all
+ *   seq_lens   [B] out: ctx_lens[b] + n_b (may be ctx_lens itself)
+ *   block_table in/out: entries ceil(ctx/page_size) .. ceil(len/page_size)-1
+ *              of row b get the next pages of free_pages [n_free], which is
+ *              used from entry *taken on, in the order of the sequences; -1
+ *              once it is used up.  Other entries are left as they were.
+ *   slot_map   [max_tokens] int64 out: page * page_size + row of each new
+ *              token, -1 where its page is missing and for the entries from
+ *              q_start[B] on (lca_append_paged skips those)
+ *   positions  [max_tokens] int32 out or NULL: the token's position in its
+ *              sequence; -1 from q_start[B] on
+ *   taken_out  [1] out: *taken plus the pages used (may be taken itself)
+ *   counts     [4] int32 out or NULL: tokens kept, tokens dropped (at most
+ *              2^31 - 1 is reported), pages used, pages missing
+ * All arrays are device memory, 4-byte aligned (slot_map: 8).  Apart from
+ * the two pairs named, no output may overlap an input or another output.
+ * B <= LCA_PAGED_MAX_BATCH, max_tokens < 2^30, max_blocks * page_size < 2^31
+ * (LCA_ERR_UNSUPPORTED otherwise). */
+#define LCA_PAGED_MAX_BATCH 8192
+int lca_page_tables(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *free_pages, int64_t n_free,
+                    const int32_t *taken, int32_t *block_table, int B, int64_t max_blocks, int page_size,
+                    int64_t max_tokens, int32_t *seq_lens, int32_t *q_start, int64_t *slot_map, int32_t *positions,
+                    int32_t *taken_out, int32_t *counts, void *stream);
+
+/* lca_append_paged: row t of rows ([T] rows of 576 bf16, row_pitch elements
+ * apart, a multiple of 8, at least 576) into slot slot_map[t] of the pages,
+ * for every slot in 0 .. n_pages*page_size-1; other slots are skipped.  Slots
+ * must be distinct (a slot given twice ends up holding vectors of either
+ * row).  T == 0 is valid. */
+int lca_append_paged(const void *rows, int64_t row_pitch, const int64_t *slot_map, int64_t T, void *pages,
+                     int64_t n_pages, int page_size, void *stream);
+
+/* mla_paged_attn: MLA attention (mla_decode_attn's formula) of every new
+ * token over its sequence's pages.  Sequence b's new tokens are rows
+ * q_start[b] .. q_start[b+1]-1 of the batch (n_b of them, none is fine); its
+ * rows, the new ones included, are already in the pages, seq_lens[b] in all.
+ * Its i-th new token sits at position seq_lens[b] - n_b + i and attends rows 0 ..
+ * position.  Rows whose page is missing are not attended; a token with no
+ * row to attend (position below 0, no page) gets zeros.
+ *   q    [T][16][576] bf16, w_uv [16][512][128] bf16
+ *   out  [T][16][128] bf16; rows that belong to no sequence (from q_start[B]
+ *        on, in a padded batch) are left as they were.
+ * Pages may hold anything in rows that no token of the call attends, NaN and
+ * infinities included.  max_new: the most new tokens any sequence may have, a hint that
+ * selects the kernel (1: single tokens); the result is right whatever it
+ * says.  Logits, softmax and sums are fp32; the softmax weights enter the
+ * value product as bf16.
+ * T < 2^27, n_pages * page_size and max_blocks * page_size < 2^31, and T *
+ * max_blocks * page_size / 64 < 2^30 (LCA_ERR_UNSUPPORTED otherwise).
+ * T == 0 is valid.  ws: mla_paged_workspace_bytes(B, T, max_new). */
+size_t mla_paged_workspace_bytes(int B, int64_t T, int max_new);
+int mla_paged_attn(const void *pages, int64_t n_pages, int page_size, const int32_t *block_table, int64_t max_blocks,
+                   const int32_t *seq_lens, const int32_t *q_start, const void *q, const void *w_uv, int B, int64_t T,
+                   int max_new, float scale, void *out, void *ws, size_t ws_bytes, void *stream);
+
 /* Self-test of the failure path (no counterpart on the page): launches one
  * kernel whose bounded wait can never be satisfied.  After ~2 s it records
  * LCA_ERR_DEVICE_TIMEOUT in the device status word (kernel id 8 in bits

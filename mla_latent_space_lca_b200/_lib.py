@@ -32,7 +32,9 @@ EXPORTS = ("lca_num_groups", "lca_workspace_bytes", "mla_decode_attn", "lca_cond
            "lca_device_status", "lca_profile_enable", "lca_profile_collect", "lca_launch_count",
            "lca_decode_noalloc", "lca_condense_append", "lca_decode_stored",
            "lca_selftest_wait_timeout", "lca_decode_shard", "lca_combine_shards", "lca_decode_varlen",
-           "lca_decode_stored_varlen", "lca_append_token")
+           "lca_decode_stored_varlen", "lca_append_token", "lca_page_tables", "lca_append_paged",
+           "mla_paged_workspace_bytes", "mla_paged_attn")
+PAGED_MAX_BATCH = 8192   # LCA_PAGED_MAX_BATCH
 # floats per head in a shard record: o (512) and its base-2 log-sum-exp
 SHARD_RECORD_PER_HEAD = 513
 
@@ -97,6 +99,14 @@ def lib():
         L.lca_decode_noalloc.argtypes = [P, P, P, P, I, I64, LcaParams, P, P, P, P]
         L.lca_prefill_block.restype = I
         L.lca_prefill_block.argtypes = [P, P, P, I, I64, I64, I64, LcaParams, P, P, P, P, SZ, P]
+        L.lca_page_tables.restype = I
+        L.lca_page_tables.argtypes = [P, P, P, I64, P, P, I, I64, I, I64, P, P, P, P, P, P, P]
+        L.lca_append_paged.restype = I
+        L.lca_append_paged.argtypes = [P, I64, P, I64, P, I64, I, P]
+        L.mla_paged_workspace_bytes.restype = SZ
+        L.mla_paged_workspace_bytes.argtypes = [I, I64, I]
+        L.mla_paged_attn.restype = I
+        L.mla_paged_attn.argtypes = [P, I64, I, P, I64, P, P, P, P, I, I64, I, F, P, P, SZ, P]
         L.lca_strerror.restype = ctypes.c_char_p
         L.lca_strerror.argtypes = [I]
         L.lca_device_status.restype = I

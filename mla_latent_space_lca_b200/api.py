@@ -350,6 +350,128 @@ def lca_append_token(cache, pos, rows, q=None, ring=None, slot=0, q_out=None, st
     check(rc, "lca_append_token")
 
 
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _pages(t):
+    _need(t, "pages", torch.bfloat16)
+    if t.dim() != 3 or t.shape[2] != D:
+        raise ValueError(f"pages has shape {tuple(t.shape)}, expected (n_pages, page_size, {D})")
+
+
+def lca_page_tables(ctx_lens, new_lens, free_pages, taken, block_table, page_size, max_tokens, seq_lens=None,
+                    q_start=None, slot_map=None, positions=None, taken_out=None, counts=None, stream=None):
+    """One step's bookkeeping of a paged cache: ctx_lens, new_lens (int32
+    [B]) and the free list (int32 [n_free], used from entry taken[0] on) ->
+    block_table (int32 [B, max_blocks], new entries written in place) and
+
+        seq_lens [B], q_start [B+1], slot_map [max_tokens] (int64),
+        positions [max_tokens], taken_out [1],
+        counts [4] = tokens kept, tokens dropped, pages used, pages missing
+
+    which are returned.  seq_lens may be ctx_lens and taken_out may be taken:
+    a serving loop then keeps its state in place.  See include/lca.h for what
+    happens when room or pages run out."""
+    _need(ctx_lens, "ctx_lens", torch.int32)
+    if ctx_lens.dim() != 1:
+        raise ValueError("ctx_lens must be [B]")
+    B, dev, n = ctx_lens.shape[0], ctx_lens.device, int(max_tokens)
+    if n < 0:
+        raise ValueError("max_tokens must not be negative")
+    _need(new_lens, "new_lens", torch.int32, (B,))
+    _need(free_pages, "free_pages", torch.int32)
+    _need(taken, "taken", torch.int32, (1,))
+    _need(block_table, "block_table", torch.int32)
+    if free_pages.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"free_pages must be [n_free] and block_table [{B}, max_blocks]")
+
+    def made(t, name, dtype, size):
+        t = torch.empty(size, dtype=dtype, device=dev) if t is None else t
+        _need(t, name, dtype, (size,))
+        return t
+
+    seq_lens = made(seq_lens, "seq_lens", torch.int32, B)
+    q_start = made(q_start, "q_start", torch.int32, B + 1)
+    slot_map = made(slot_map, "slot_map", torch.int64, n)
+    positions = made(positions, "positions", torch.int32, n)
+    taken_out = made(taken_out, "taken_out", torch.int32, 1)
+    counts = made(counts, "counts", torch.int32, 4)
+    _same_device(ctx_lens, new_lens=new_lens, free_pages=free_pages, taken=taken, block_table=block_table,
+                 seq_lens=seq_lens, q_start=q_start, slot_map=slot_map, positions=positions, taken_out=taken_out,
+                 counts=counts)
+    with torch.cuda.device(dev):
+        rc = _lib.lib().lca_page_tables(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages), free_pages.numel(),
+                                        _ptr(taken), _ptr(block_table), B, block_table.shape[1], int(page_size), n,
+                                        _ptr(seq_lens), _ptr(q_start), _ptr(slot_map), _ptr(positions),
+                                        _ptr(taken_out), _ptr(counts), _stream(stream))
+    check(rc, "lca_page_tables")
+    return seq_lens, q_start, slot_map, positions, taken_out, counts
+
+
+def lca_append_paged(pages, rows, slot_map, stream=None):
+    """rows [T, 576] (bf16, rows may lie apart: a slice of a wider tensor)
+    into pages [n_pages, page_size, 576] at slots slot_map [T] (int64,
+    page * page_size + row); slots outside the pages, such as -1, are
+    skipped.  Slots must be distinct."""
+    _pages(pages)
+    if not isinstance(rows, torch.Tensor) or not rows.is_cuda or rows.dtype != torch.bfloat16:
+        raise TypeError("rows must be a CUDA bfloat16 tensor")
+    if rows.dim() != 2 or rows.shape[1] != D:
+        raise ValueError(f"rows has shape {tuple(rows.shape)}, expected (T, {D})")
+    T = rows.shape[0]
+    pitch = rows.stride(0) if T > 1 else D
+    if rows.stride(1) != 1 or pitch < D:
+        raise ValueError(f"rows must not overlap and hold contiguous vectors (strides {rows.stride()})")
+    _need(slot_map, "slot_map", torch.int64, (T,))
+    _same_device(pages, rows=rows, slot_map=slot_map)
+    with torch.cuda.device(pages.device):
+        rc = _lib.lib().lca_append_paged(_ptr(rows), pitch, _ptr(slot_map), T, _ptr(pages), pages.shape[0],
+                                         pages.shape[1], _stream(stream))
+    check(rc, "lca_append_paged")
+
+
+def paged_workspace(B: int, T: int, max_new: int, device=None) -> torch.Tensor:
+    """Scratch for mla_paged_attn on a batch of B sequences and T tokens."""
+    n = int(_lib.lib().mla_paged_workspace_bytes(B, T, max_new))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def mla_paged_attn(pages, block_table, seq_lens, q_start, q, w_uv, max_new, scale=None, out=None, ws=None,
+                   stream=None):
+    """MLA attention of each sequence's new tokens (rows q_start[b] ..
+    q_start[b+1]-1 of q [T, 16, 576]) over its rows in pages
+    [n_pages, page_size, 576], block_table [B, max_blocks]; seq_lens [B]
+    counts the new tokens' rows too, which are in the pages already.
+    Returns out [T, 16, 128] bf16.  max_new: the most new tokens that any
+    sequence has; 1 selects the single-token form."""
+    _pages(pages)
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B = block_table.shape[0]
+    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(q_start, "q_start", torch.int32, (B + 1,))
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 3 or tuple(q.shape[1:]) != (H, D):
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected (T, {H}, {D})")
+    T = q.shape[0]
+    _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
+    out = torch.empty(T, H, D_V, dtype=torch.bfloat16, device=q.device) if out is None else out
+    _need(out, "out", torch.bfloat16, (T, H, D_V))
+    ws = paged_workspace(B, T, max_new, device=q.device) if ws is None else ws
+    _same_device(pages, block_table=block_table, seq_lens=seq_lens, q_start=q_start, q=q, w_uv=w_uv, out=out, ws=ws)
+    with torch.cuda.device(pages.device):
+        rc = _lib.lib().mla_paged_attn(_ptr(pages), pages.shape[0], pages.shape[1], _ptr(block_table),
+                                       block_table.shape[1], _ptr(seq_lens), _ptr(q_start), _ptr(q), _ptr(w_uv), B, T,
+                                       int(max_new), float(default_scale() if scale is None else scale), _ptr(out),
+                                       _ptr(ws), ws.numel(), _stream(stream))
+    check(rc, "mla_paged_attn")
+    return out
+
+
 def device_status(clear: bool = True) -> tuple[int, int]:
     d = ctypes.c_int(0)
     rc = _lib.lib().lca_device_status(1 if clear else 0, ctypes.byref(d))

@@ -109,6 +109,61 @@ struct AttnArgs {
     // launch only once everything before it in the stream has completed, so
     // the cache may be read without waiting for the summary query
     int after_prep;
+    // paged cache only: "sequence" b above is one token of the batch (its
+    // query row, lens[b] = the rows it attends), whose rows are those of
+    // sequence item_seq[b], row r in page block_table[item_seq[b]][r >> page_shift]
+    const int32_t *item_seq;
+    const int32_t *block_table;
+    int64_t max_blocks;
+    int64_t n_pages;
+    int page_shift;
+};
+
+// Shared-memory layout of a 64-row tile.  A contiguous cache's tile arrives as
+// nine [64 rows x 64 columns] blocks.  A paged cache's tile arrives page by
+// page, as [8 groups of 8 rows][9 chunks of 64 columns][8 rows x 128 B]: the
+// stride between two 8-row groups is the same inside a page and across pages,
+// so one matrix descriptor covers a tile whatever the page size.
+template <bool PAGED>
+struct TileLayout {
+    static constexpr int kChunk = PAGED ? 1024 : AT_CHUNK;        // between 64-column chunks
+    static constexpr int kGroup = PAGED ? 9 * 1024 : 1024;        // between 8-row groups
+    static __device__ __forceinline__ uint32_t row(int r) { return (r >> 3) * kGroup + (r & 7) * 128; }
+};
+
+// Entry of a block table at page index k of a row of max_blocks entries, or
+// -1 (no page) past the row's end or where the entry names no page.
+__device__ __forceinline__ int32_t page_entry(const int32_t *row, int64_t k, int64_t max_blocks, int64_t n_pages)
+{
+    const int32_t e = k < max_blocks ? __ldg(row + k) : -1;
+    return e >= 0 && int64_t(e) < n_pages ? e : -1;
+}
+
+// A warp's view of one block-table row, walked forwards: lane i holds entry
+// base + i, and the next 32 entries are already on their way.
+struct PageWindow {
+    const int32_t *row = nullptr;
+    int64_t base = 0, max_blocks, n_pages;
+    int32_t cur, nxt;
+    __device__ __forceinline__ void open(const int32_t *r, int64_t first, int64_t mb, int64_t np, int lane)
+    {
+        row = r;
+        base = first;
+        max_blocks = mb;
+        n_pages = np;
+        cur = page_entry(row, base + lane, mb, np);
+        nxt = page_entry(row, base + 32 + lane, mb, np);
+    }
+    // entry k (base <= k < base + 64), the same for the whole warp
+    __device__ __forceinline__ int32_t at(int64_t k, int lane)
+    {
+        if (k >= base + 32) {
+            base += 32;
+            cur = nxt;
+            nxt = page_entry(row, base + 32 + lane, max_blocks, n_pages);
+        }
+        return __shfl_sync(0xffffffffu, cur, int(k - base));
+    }
 };
 
 // Geometry of one sequence of L rows: its groups m, first window row and
@@ -283,11 +338,13 @@ __device__ __forceinline__ void load_q_rows(const uint16_t *qb, const uint16_t *
     }
 }
 
-template <int MODE, bool VARLEN = false>
+template <int MODE, bool VARLEN = false, bool PAGED = false>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_cache,
                        const __grid_constant__ CUtensorMap map_rep, const AttnArgs a)
 {
+    static_assert(!PAGED || (MODE == MODE_MLA && VARLEN), "pages: plain rows of a ragged batch");
+    using Lay = TileLayout<PAGED>;
     extern __shared__ uint8_t at_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(at_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -309,6 +366,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + AT_OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + AT_OFF_MISC + 4);
     float *fsc = reinterpret_cast<float *>(smem + AT_OFF_MISC + 128);   // [2][16]
+    volatile uint32_t *held = reinterpret_cast<volatile uint32_t *>(smem + AT_OFF_MISC + 8);   // paged: [3] per stage
     float *alb = reinterpret_cast<float *>(smem + AT_OFF_ALB) + AT_ALB * (warp & 3);   // this softmax warp's
 
     if (threadIdx.x == 0) {
@@ -355,7 +413,72 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     const int64_t t_begin = split_begin(c, T, a.G);
     const int64_t t_end = split_begin(c + 1, T, a.G);
 
-    if (warp == 5) {
+    if (PAGED && warp == 5) {
+        // ------------------------------------------------------------ TMA producer, pages
+        // The whole warp walks the block table; lane 0 issues the copies, one
+        // per page (or per tile, where a page holds several).  Rows of a page
+        // that the table does not name come from beyond the tensor map, which
+        // fills zeros, and `held` tells the softmax warps to mask them.
+        const uint64_t pol = policy_evict_first();
+        const bool staged = t_begin < t_end;
+        SeqTiles sq{};
+        sq.b = -1;
+        if (staged) sq = seq_of<MODE, VARLEN>(a, t_begin, sq);
+        if (lane == 0) {
+            prefetch_tensormap(&map_cache);
+            if (staged) {
+                mbar_expect_tx(qfull, AT_QBYTES);
+                bulk_load(sbase + AT_OFF_QSTAGE, a.q + size_t(sq.b) * LCA_HEADS * LCA_D, AT_QBYTES, qfull,
+                          policy_evict_last());
+            }
+        }
+        const int sub_shift = min(a.page_shift, 6);   // rows per copy: min(page, 64)
+        const int copies = AT_TILE >> sub_shift;
+        const int64_t no_page = a.n_pages << (a.page_shift - 3);   // a group beyond the map
+        PageWindow win;
+        int last[3] = {-1, -1, -1};
+        int i = 0;
+        int64_t open_b = -1;
+        for (int64_t t = t_begin; t < t_end; ++t, ++i) {
+            const int s = i % 3;
+            sq = seq_of<MODE, VARLEN>(a, t, sq);
+            const int64_t row0 = (t - sq.t0) * AT_TILE;
+            if (sq.b != open_b) {
+                open_b = sq.b;
+                win.open(a.block_table + size_t(a.item_seq[sq.b]) * size_t(a.max_blocks), row0 >> a.page_shift,
+                         a.max_blocks, a.n_pages, lane);
+            }
+            bool ok = true;
+            if (i == 2) ok = mbar_wait(qempty, 0, abort_flag, K_ATTN, 14);
+            ok = ok && mbar_wait(empty(s), ((i / 3) & 1) ^ 1, abort_flag, K_ATTN, 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            uint32_t mask = 0;
+            int64_t group[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k < copies) {
+                    const int64_t r = row0 + (int64_t(k) << sub_shift);
+                    const int32_t page = win.at(r >> a.page_shift, lane);
+                    if (page >= 0) mask |= 1u << k;
+                    group[k] = page >= 0 ? ((int64_t(page) << a.page_shift) + (r & ((int64_t(1) << a.page_shift) - 1))) >> 3
+                                         : no_page;
+                }
+            }
+            if (lane == 0) {
+                held[s] = mask;
+                mbar_expect_tx(full(s), AT_STAGE);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < copies)
+                        tma_load_4d(sbase + s * AT_STAGE + ((k << sub_shift) >> 3) * Lay::kGroup, &map_cache, full(s), 0,
+                                    0, 0, int(group[k]), pol);
+            }
+            last[s] = i;
+        }
+        for (int s = 0; s < 3; ++s)
+            if (last[s] >= 0) mbar_wait(full(s), (last[s] / 3) & 1, nullptr, K_ATTN, 2);
+        if (staged) mbar_wait(qfull, 0, nullptr, K_ATTN, 15);   // no copy left in flight
+    } else if (warp == 5) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             prefetch_tensormap(&map_cache);
@@ -419,7 +542,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll 6
                 for (int ks = 0; ks < 18; ++ks) {
                     const int kg = 18 * half + ks;
-                    const uint64_t bd = sdesc_sw128(stage + (kg >> 2) * AT_CHUNK + (kg & 3) * 32, 16, 1024);
+                    const uint64_t bd = sdesc_sw128(stage + (kg >> 2) * Lay::kChunk + (kg & 3) * 32, 16, Lay::kGroup);
                     mma_ts(dS, tmem + AT_TM_Q + 8 * ks, bd, IDESC_S, ks > 0 ? 1u : 0u);
                 }
                 tc_commit(sfull(i & 1));
@@ -449,7 +572,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                 const uint32_t pbuf = sbase + AT_OFF_P + (j & 1) * AT_PBUF;
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t ad = sdesc_sw128(stage + 2 * cc * AT_CHUNK + ks * 2048, AT_CHUNK, 1024);
+                    const uint64_t ad = sdesc_sw128(stage + 2 * cc * Lay::kChunk + ks * 2 * Lay::kGroup, Lay::kChunk, Lay::kGroup);
                     const uint64_t bd = sdesc_sw128(pbuf + ks * 32, 16, 1024);
                     mma_ss(tmem + AT_TM_O + 16 * cc, ad, bd, IDESC_PV, (j == first_j && ks == 0) ? 0u : 1u);
                 }
@@ -508,6 +631,13 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                 const TileInfo ti = tile_info<MODE>(sq.g, k);
                 ok = mbar_wait(sfull(sb), (i >> 1) & 1, abort_flag, K_ATTN, 8);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                uint32_t pmask = 0xfu;   // which of the tile's page pieces are there
+                if constexpr (PAGED) {
+                    // complete already: S has read the tile
+                    ok = mbar_wait(full(i % 3), (i / 3) & 1, abort_flag, K_ATTN, 17);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    pmask = held[i % 3];
+                }
                 tc_fence_after();
                 // thread T: rows g = T/4 (lo) and g+8 (hi), tokens
                 // tok(x) = 8*(x>>1) + 2*sub + (x&1), x = 0..15; group of x = x>>2
@@ -550,7 +680,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                         uint8_t *stg = smem + (i % 3) * AT_STAGE;
                         for (int x = 32 * quad + lane; x < 8 * nr * 8; x += 128) {
                             const int box = x / (8 * nr), r = ok_rows + (x / 8) % nr, ch = x % 8;
-                            *reinterpret_cast<uint4 *>(stg + box * AT_CHUNK + r * 128 + ch * 16) =
+                            *reinterpret_cast<uint4 *>(stg + box * Lay::kChunk + Lay::row(r) + ch * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
@@ -693,11 +823,14 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
                         const int tok = 8 * (x >> 1) + 2 * sub + (x & 1);
-                        w[x] = (tok < ti.valid) ? lo[x] * a.sl2 : NEG_INF;
+                        bool in = tok < ti.valid;
+                        if constexpr (PAGED) in = in && ((pmask >> (tok >> min(a.page_shift, 6))) & 1u);
+                        w[x] = in ? lo[x] * a.sl2 : NEG_INF;
                         tmax = fmaxf(tmax, w[x]);
                     }
                     tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
                     tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
+                    if constexpr (PAGED) tmax = fmaxf(tmax, -1e30f);   // a tile without any page
                     if (i == first) {
                         m_use = tmax;
                     } else if (tmax > m_use + 8.f) {

@@ -23,6 +23,7 @@
 #include "selftest.cuh"
 #include "varlen.cuh"
 #include "append.cuh"
+#include "paged.cuh"
 
 using namespace lca;
 
@@ -68,10 +69,13 @@ int current_device(DeviceInfo **out)
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_MLA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_LCA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_REPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_MLA, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(tail_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TD_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(tables_smem(TB_MAX_BATCH))) == cudaSuccess;
         good &= cudaFuncSetAttribute(condense_kernel<CdShape::kWarps, CdShape::kSlots>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, CdShape::kSmem) == cudaSuccess;
         good &= cudaFuncSetAttribute(wuv_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM_ALLOC) == cudaSuccess;
-        good &= cudaFuncSetAttribute(tail_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TD_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(tail_decode_kernel<>, cudaFuncAttributeMaxDynamicSharedMemorySize, TD_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(condense_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CP_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AP_SMEM_ALLOC) == cudaSuccess;
         // One shared-memory carveout (the largest) for every kernel of the
@@ -87,7 +91,12 @@ int current_device(DeviceInfo **out)
         good &= carve(reinterpret_cast<const void *>(attn_decode_kernel<MODE_MLA, true>));
         good &= carve(reinterpret_cast<const void *>(attn_decode_kernel<MODE_LCA, true>));
         good &= carve(reinterpret_cast<const void *>(attn_decode_kernel<MODE_REPS, true>));
-        good &= carve(reinterpret_cast<const void *>(tail_decode_kernel));
+        good &= carve(reinterpret_cast<const void *>(tail_decode_kernel<>));
+        good &= carve(reinterpret_cast<const void *>(attn_decode_kernel<MODE_MLA, true, true>));
+        good &= carve(reinterpret_cast<const void *>(tail_decode_kernel<true>));
+        good &= carve(reinterpret_cast<const void *>(paged_plan_kernel));
+        good &= carve(reinterpret_cast<const void *>(append_paged_kernel));
+        good &= carve(reinterpret_cast<const void *>(page_tables_kernel));
         good &= carve(reinterpret_cast<const void *>(prep_summary_kernel));
         good &= carve(reinterpret_cast<const void *>(append_token_kernel));
         good &= carve(reinterpret_cast<const void *>(condense_kernel<CdShape::kWarps, CdShape::kSlots>));
@@ -162,14 +171,30 @@ int make_map_reps(CUtensorMap *m, const void *base, uint64_t nbc, uint64_t group
     return r == CUDA_SUCCESS ? LCA_OK : LCA_ERR_CUDA;
 }
 
+// Pages of [page][576] bf16 as a 4-D tensor (column within a 64-column chunk,
+// row within a group of 8, chunk, group): a box of [groups][chunks][8][64]
+// lands as whole 8 x 128 B swizzle atoms, chunk after chunk, group after group.
+int make_map_pages(CUtensorMap *m, const void *base, uint64_t rows, uint32_t box_rows, uint32_t box_chunks)
+{
+    cuuint64_t dims[4] = {64, 8, LCA_D / 64, rows / 8};
+    cuuint64_t strides[3] = {uint64_t(LCA_D) * 2, 128, uint64_t(LCA_D) * 2 * 8};
+    cuuint32_t box[4] = {64, 8, box_chunks, box_rows / 8};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides,
+                          box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? LCA_OK : LCA_ERR_CUDA;
+}
+
 // ------------------------------------------------------------------ timing / counting
 struct ProfRec {
     cudaEvent_t a, b;
     int kid;
 };
 const char *kKernelNames[] = {"",         "prep_summary", "condense",    "attn_decode",      "combine_wuv",
-                               "wuv_gemm", "attn_prefill", "condense_prefill", "selftest_wait", "append_token"};
-constexpr int kNumKernelIds = 10;
+                               "wuv_gemm", "attn_prefill", "condense_prefill", "selftest_wait", "append_token",
+                               "page_tables", "append_paged", "paged_plan"};
+constexpr int kNumKernelIds = 13;
 bool g_prof_on = false;
 std::vector<ProfRec> g_prof_used;
 std::vector<std::pair<cudaEvent_t, cudaEvent_t>> g_prof_pool;
@@ -417,10 +442,11 @@ int run_attention(DeviceInfo *dev, const void *cache, const void *rep, const voi
         Launch l(st, K_COMBINE);
         // rows per CTA: enough CTAs (16 heads x row groups) to cover the SMs
         const int rpc = std::max(1, std::min(TD_ROWS, (LCA_HEADS * B + dev->sms - 1) / dev->sms));
-        const cudaError_t e = launch_ex(tail_decode_kernel, dim3(LCA_HEADS, (B + rpc - 1) / rpc), dim3(256),
+        const cudaError_t e = launch_ex(tail_decode_kernel<>, dim3(LCA_HEADS, (B + rpc - 1) / rpc), dim3(256),
                                         TD_SMEM_ALLOC, st, true, map_w, (const float *)w.part_o,
                                         (const float *)w.part_ml, B, a.n_tiles, a.T, a.G, o_lat, out, rpc,
-                                        lse_out, 0, int64_t(0), (const int32_t *)a.tile_start);
+                                        lse_out, 0, int64_t(0), (const int32_t *)a.tile_start,
+                                        (uint16_t *)nullptr, (const int32_t *)nullptr);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     return LCA_OK;
@@ -435,6 +461,107 @@ int launch_prep(const void *q_recent, int B, const lca_params &p, const DecodeWs
                                     int64_t(p.g) * LCA_HEADS * LCA_D, coef, w.u, w.uhl);
     if (e != cudaSuccess) return LCA_ERR_CUDA;
     return l.done();
+}
+
+// ------------------------------------------------------------------ paged cache
+// log2 of a page size the kernels take (a power of two from 16), or -1.
+int page_shift(int page_size)
+{
+    for (int s = 4; s <= 16; ++s)
+        if (page_size == (1 << s)) return s;
+    return -1;
+}
+
+// Workspace of the attention over pages: the work list and, for each piece of
+// a token's rows, its partial output.
+struct PagedWs {
+    int32_t *item_seq, *item_len, *tile_start;
+    float *part_o, *part_ml;
+    size_t bytes;
+};
+
+PagedWs paged_ws_layout(void *ws, int64_t T)
+{
+    PagedWs w{};
+    const size_t n = size_t(T), slots = size_t(kMaxCtas) + n;
+    size_t off[6];
+    off[0] = 0;
+    off[1] = off[0] + align_up(n * 4);                                  // item_seq
+    off[2] = off[1] + align_up(n * 4);                                  // item_len
+    off[3] = off[2] + align_up((n + 1) * 4);                            // tile_start
+    off[4] = off[3] + align_up(slots * LCA_HEADS * LCA_DC * 4);          // part_o
+    off[5] = off[4] + align_up(slots * LCA_HEADS * 2 * 4);               // part_ml
+    w.bytes = off[5];
+    if (ws) {
+        uint8_t *p = static_cast<uint8_t *>(ws);
+        w.item_seq = reinterpret_cast<int32_t *>(p + off[0]);
+        w.item_len = reinterpret_cast<int32_t *>(p + off[1]);
+        w.tile_start = reinterpret_cast<int32_t *>(p + off[2]);
+        w.part_o = reinterpret_cast<float *>(p + off[3]);
+        w.part_ml = reinterpret_cast<float *>(p + off[4]);
+    }
+    return w;
+}
+
+struct PagedCall {
+    const void *pages, *q, *w_uv;
+    int64_t n_pages, max_blocks, T;
+    const int32_t *block_table, *seq_lens, *q_start;
+    int B, shift;
+    float scale;
+    void *out;
+    cudaStream_t st;
+};
+
+// Every token an item of its own: the split-L decode attention over its rows.
+int run_paged_tokens(DeviceInfo *dev, const PagedCall &c, const PagedWs &w)
+{
+    int rc = get_encode();
+    if (rc) return rc;
+    const int64_t max_rows = c.max_blocks << c.shift;
+    const int T = int(c.T);
+    {
+        Launch l(c.st, K_PAGED_PLAN);
+        const cudaError_t e = launch_ex(paged_plan_kernel, dim3(1), dim3(1024), 0, c.st, true, c.seq_lens, c.q_start,
+                                        c.B, T, max_rows, w.item_seq, w.item_len, w.tile_start);
+        if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
+    }
+    CUtensorMap map_pages, map_w;
+    rc = make_map_pages(&map_pages, c.pages, uint64_t(c.n_pages) << c.shift, std::min(1 << c.shift, AT_TILE), LCA_D / 64);
+    if (rc) return rc;
+    rc = make_map3(&map_w, c.w_uv, LCA_DV, LCA_DC, LCA_HEADS, LCA_DV * 2, LCA_DC * LCA_DV * 2, 64, 64, 1);
+    if (rc) return rc;
+    AttnArgs a{};
+    a.q = static_cast<const uint16_t *>(c.q);
+    a.L = max_rows;
+    a.G = std::min(dev->sms, kMaxCtas);
+    a.sl2 = c.scale * 1.4426950408889634f;
+    a.part_o = w.part_o;
+    a.part_ml = w.part_ml;
+    a.lens = w.item_len;
+    a.tile_start = w.tile_start;
+    a.B = T;
+    a.item_seq = w.item_seq;
+    a.block_table = c.block_table;
+    a.max_blocks = c.max_blocks;
+    a.n_pages = c.n_pages;
+    a.page_shift = c.shift;
+    {
+        Launch l(c.st, K_ATTN);
+        const cudaError_t e = launch_ex(attn_decode_kernel<MODE_MLA, true, true>, dim3(a.G), dim3(AT_THREADS),
+                                        AT_SMEM_ALLOC, c.st, true, map_pages, map_pages, a);
+        if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
+    }
+    Launch l(c.st, K_COMBINE);
+    const int rpc = int(std::max<int64_t>(1, std::min<int64_t>(TD_ROWS, (LCA_HEADS * c.T + dev->sms - 1) / dev->sms)));
+    const cudaError_t e = launch_ex(tail_decode_kernel<true>, dim3(LCA_HEADS, (T + rpc - 1) / rpc), dim3(256),
+                                    TD_SMEM_ALLOC, c.st, true, map_w, (const float *)w.part_o,
+                                    (const float *)w.part_ml, T, 0, int64_t(0), a.G, (float *)nullptr,
+                                    (float *)nullptr, rpc, (float *)nullptr, 0, int64_t(0),
+                                    (const int32_t *)w.tile_start, static_cast<uint16_t *>(c.out),
+                                    (const int32_t *)w.item_len);
+    if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
+    return LCA_OK;
 }
 
 // ------------------------------------------------------------------ no-allocation decode
@@ -773,10 +900,10 @@ int lca_combine_shards(const float *parts, int n_shards, int B, const void *w_uv
     Launch l(st, K_COMBINE);
     const int rpc = std::max(1, std::min(TD_ROWS, (LCA_HEADS * B + dev->sms - 1) / dev->sms));
     const int64_t stride = int64_t(B) * LCA_HEADS * LCA_SHARD_RECORD_PER_HEAD;
-    const cudaError_t e = launch_ex(tail_decode_kernel, dim3(LCA_HEADS, (B + rpc - 1) / rpc), dim3(256),
+    const cudaError_t e = launch_ex(tail_decode_kernel<>, dim3(LCA_HEADS, (B + rpc - 1) / rpc), dim3(256),
                                     TD_SMEM_ALLOC, st, false, map_w, parts, (const float *)nullptr, B, 0,
                                     int64_t(0), 0, o_lat, out, rpc, (float *)nullptr, n_shards, stride,
-                                    (const int32_t *)nullptr);
+                                    (const int32_t *)nullptr, (uint16_t *)nullptr, (const int32_t *)nullptr);
     if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     return LCA_OK;
 }
@@ -916,6 +1043,106 @@ int lca_append_token(const void *rows, void *cache, int B, int64_t pitch, int64_
                                     static_cast<uint4 *>(q_dst));
     if (e != cudaSuccess) return LCA_ERR_CUDA;
     return l.done();
+}
+
+int lca_page_tables(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *free_pages, int64_t n_free,
+                    const int32_t *taken, int32_t *block_table, int B, int64_t max_blocks, int page_size,
+                    int64_t max_tokens, int32_t *seq_lens, int32_t *q_start, int64_t *slot_map, int32_t *positions,
+                    int32_t *taken_out, int32_t *counts, void *stream)
+{
+    if (!ctx_lens || !new_lens || !taken || !block_table || !seq_lens || !q_start || !taken_out) return LCA_ERR_INVALID_ARG;
+    if (B < 1 || max_blocks < 1 || page_size < 1 || max_tokens < 0 || n_free < 0 || n_free > 0x7fffffff)
+        return LCA_ERR_INVALID_ARG;
+    if ((n_free > 0 && !free_pages) || (max_tokens > 0 && !slot_map)) return LCA_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (shift < 0 || B > LCA_PAGED_MAX_BATCH || max_tokens >= (int64_t(1) << 30) ||
+        max_blocks > (int64_t(0x7fffffff) >> shift))
+        return LCA_ERR_UNSUPPORTED;
+    for (const void *p : {(const void *)ctx_lens, (const void *)new_lens, (const void *)free_pages, (const void *)taken,
+                          (const void *)block_table, (const void *)seq_lens, (const void *)q_start,
+                          (const void *)positions, (const void *)taken_out, (const void *)counts})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return LCA_ERR_MISALIGNED;
+    if (reinterpret_cast<uintptr_t>(slot_map) & 7u) return LCA_ERR_MISALIGNED;
+    DeviceInfo *dev = nullptr;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    TablesArgs a{ctx_lens, new_lens, free_pages, taken, n_free, block_table, B, max_blocks, shift, int32_t(max_tokens),
+                 seq_lens, q_start, slot_map, positions, taken_out, counts};
+    cudaLaunchConfig_t cfg{};
+    const unsigned ctas = max_tokens > 2048 ? 8 : 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(1024);
+    cfg.dynamicSmemBytes = tables_smem(B);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    Launch l(cfg.stream, K_TABLES);
+    if (cudaLaunchKernelEx(&cfg, page_tables_kernel, a) != cudaSuccess) return LCA_ERR_CUDA;
+    return l.done();
+}
+
+int lca_append_paged(const void *rows, int64_t row_pitch, const int64_t *slot_map, int64_t T, void *pages,
+                     int64_t n_pages, int page_size, void *stream)
+{
+    if (T < 0 || n_pages < 1 || page_size < 1 || row_pitch < LCA_D || !pages || (T > 0 && (!rows || !slot_map)))
+        return LCA_ERR_INVALID_ARG;
+    if (page_shift(page_size) < 0) return LCA_ERR_UNSUPPORTED;
+    if (n_pages >= (int64_t(1) << 40) / page_size || T >= (int64_t(1) << 40) || row_pitch >= (int64_t(1) << 40))
+        return LCA_ERR_INVALID_ARG;
+    if (!aligned16(rows) || !aligned16(pages) || (row_pitch & 7) || (reinterpret_cast<uintptr_t>(slot_map) & 7u))
+        return LCA_ERR_MISALIGNED;
+    if (T == 0) return LCA_OK;
+    DeviceInfo *dev = nullptr;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    const int64_t want = (T + AP_ROWS - 1) / AP_ROWS;
+    const int grid = int(std::min<int64_t>(want, int64_t(dev->sms) * 28));   // 7 CTAs of 288 threads an SM, 4 passes
+    Launch l(static_cast<cudaStream_t>(stream), K_APPEND_PAGED);
+    const cudaError_t e = launch_ex(append_paged_kernel, dim3(grid), dim3(APG_THREADS), 0,
+                                    static_cast<cudaStream_t>(stream), true, static_cast<const uint16_t *>(rows),
+                                    row_pitch, slot_map, T, static_cast<uint4 *>(pages), n_pages * page_size);
+    if (e != cudaSuccess) return LCA_ERR_CUDA;
+    return l.done();
+}
+
+size_t mla_paged_workspace_bytes(int B, int64_t T, int max_new)
+{
+    if (B < 1 || T < 1 || max_new < 1 || T >= (int64_t(1) << 27)) return 0;
+    return paged_ws_layout(nullptr, T).bytes;
+}
+
+int mla_paged_attn(const void *pages, int64_t n_pages, int page_size, const int32_t *block_table, int64_t max_blocks,
+                   const int32_t *seq_lens, const int32_t *q_start, const void *q, const void *w_uv, int B, int64_t T,
+                   int max_new, float scale, void *out, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!pages || !block_table || !seq_lens || !q_start || !w_uv || (T > 0 && (!q || !out))) return LCA_ERR_INVALID_ARG;
+    if (B < 1 || T < 0 || n_pages < 1 || page_size < 1 || max_blocks < 1 || max_new < 1) return LCA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || scale <= 0.f) return LCA_ERR_INVALID_ARG;
+    const int shift = page_shift(page_size);
+    if (shift < 0 || n_pages > (int64_t(0x7fffffff) >> shift) || max_blocks > (int64_t(0x7fffffff) >> shift) ||
+        T >= (int64_t(1) << 27))
+        return LCA_ERR_UNSUPPORTED;
+    // tile offsets are int32: every token's tiles together must stay below 2^30
+    if (T * (((max_blocks << shift) + AT_TILE - 1) / AT_TILE) >= (int64_t(1) << 30)) return LCA_ERR_UNSUPPORTED;
+    if (!aligned16(pages) || !aligned16(q) || !aligned16(w_uv) || !aligned16(out)) return LCA_ERR_MISALIGNED;
+    for (const int32_t *p : {block_table, seq_lens, q_start})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return LCA_ERR_MISALIGNED;
+    if (T == 0) return LCA_OK;
+    const PagedWs w = paged_ws_layout(ws, T);
+    int rc = check_ws(ws, ws_bytes, w.bytes);
+    if (rc) return rc;
+    DeviceInfo *dev = nullptr;
+    if ((rc = current_device(&dev))) return rc;
+    const PagedCall c{pages, q, w_uv, n_pages, max_blocks, T, block_table, seq_lens, q_start, B, shift, scale, out,
+                      static_cast<cudaStream_t>(stream)};
+    return run_paged_tokens(dev, c, w);
 }
 
 int lca_selftest_wait_timeout(void *stream)

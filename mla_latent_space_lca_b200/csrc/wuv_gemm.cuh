@@ -147,6 +147,13 @@ __global__ void __launch_bounds__(128, 1)
 //    a slot with maximum lse2 and denominator 1.
 // For a ragged batch tile_start (B+1 offsets into the batch's tile list)
 // replaces the uniform b * n_tiles.
+// PAGED (a ragged batch whose "sequences" are single tokens over pages):
+// out16 takes the result in bf16.  o enters the product as two bf16 values,
+// o = hi + lo, lo in the operand's unused rows 8..15, so that the only
+// roundings to bf16 between logits and result are the weights' and the
+// result's own.  A token with no row to attend (no tiles, or every page
+// missing) gets zeros; a row that belongs to no token (item_len < 0) is left
+// as it was.
 constexpr int TD_ROWS = 8;
 constexpr int TD_N = 16;
 constexpr int TD_A = LCA_DC * LCA_DV * 2;               // 131072
@@ -159,12 +166,14 @@ constexpr int TD_OFF_BAR = TD_OFF_COEF + TD_ROWS * 8 * 4;
 constexpr int TD_SMEM = TD_OFF_BAR + 256;
 constexpr int TD_SMEM_ALLOC = TD_SMEM + 1024;
 
+template <bool PAGED = false>
 __global__ void __launch_bounds__(256, 1)
     tail_decode_kernel(const __grid_constant__ CUtensorMap map_w, const float *__restrict__ part_o,
                        const float *__restrict__ part_ml, int B, int n_tiles, int64_t T, int G,
                        float *__restrict__ o_lat, float *__restrict__ out, int rpc,
                        float *__restrict__ lse_out, int n_shards, int64_t shard_stride,
-                       const int32_t *__restrict__ tile_start)
+                       const int32_t *__restrict__ tile_start, uint16_t *__restrict__ out16 = nullptr,
+                       const int32_t *__restrict__ item_len = nullptr)
 {
     extern __shared__ uint8_t td_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -175,7 +184,7 @@ __global__ void __launch_bounds__(256, 1)
     const int b0 = blockIdx.y * rpc;           // rpc <= TD_ROWS rows (sequences) per CTA
     const int nb = min(rpc, B - b0);
     const int wpr = max(1, TD_ROWS / nb);     // warps per row
-    const bool gemm = out != nullptr;
+    const bool gemm = PAGED || out != nullptr;
     const size_t lse_off = size_t(B) * LCA_HEADS * LCA_DC;   // lse2 within a shard record
     const uint32_t wbar = sbase + TD_OFF_BAR, accf = wbar + 8, drain0 = wbar + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + TD_OFF_BAR + 128);
@@ -231,10 +240,14 @@ __global__ void __launch_bounds__(256, 1)
             const int b = b0 + r;
             if (tile_start && !n_shards) {
                 TT = tile_start[B];
-                c0 = split_owner(int64_t(tile_start[b]), TT, G);
-                ns = split_owner(int64_t(tile_start[b + 1]) - 1, TT, G) - c0 + 1;
+                if (PAGED && tile_start[b + 1] == tile_start[b]) {
+                    ns = 0;   // no tile, no slot
+                } else {
+                    c0 = split_owner(int64_t(tile_start[b]), TT, G);
+                    ns = split_owner(int64_t(tile_start[b + 1]) - 1, TT, G) - c0 + 1;
+                }
             }
-            const int mine = (ns - sub + wpr - 1) / wpr;   // slots sub, sub+wpr, ...
+            const int mine = max(0, (ns - sub + wpr - 1) / wpr);   // slots sub, sub+wpr, ...
             auto slot_vec = [&](int k) {   // this lane's 16 floats of the warp's k-th slot
                 const int s = sub + wpr * k;
                 const float *rec = n_shards ? part_o + size_t(s) * shard_stride + (size_t(b) * LCA_HEADS + h) * LCA_DC
@@ -342,6 +355,7 @@ __global__ void __launch_bounds__(256, 1)
         float dt = f * di;
 #pragma unroll
         for (int off = 4; off; off >>= 1) dt += __shfl_xor_sync(0xffffffffu, dt, off);
+        if (PAGED && dt == 0.f) dt = 1.f;   // nothing attended: o = 0
         if (lane < wpr) coef[rr * 8 + lane] = f * (1.f / dt);
         if (lse_out && lane == 0) lse_out[size_t(b0 + rr) * LCA_HEADS + h] = Mt + log2f(dt);
     }
@@ -368,7 +382,11 @@ __global__ void __launch_bounds__(256, 1)
         }
         const int unit = (k & 63) >> 3, within = (k & 7) * 2;
         uint8_t *rowp = smem + TD_OFF_B + (k >> 6) * TD_BCHUNK + (r >> 3) * 1024 + (r & 7) * 128;
-        *reinterpret_cast<uint32_t *>(rowp + ((unit ^ (r & 7)) << 4) + within) = pack_bf16(o0, o1);
+        const uint32_t hi = pack_bf16(o0, o1);
+        *reinterpret_cast<uint32_t *>(rowp + ((unit ^ (r & 7)) << 4) + within) = hi;
+        if constexpr (PAGED)   // row 8 + r
+            *reinterpret_cast<uint32_t *>(rowp + 1024 + ((unit ^ (r & 7)) << 4) + within) =
+                pack_bf16(o0 - bf_lo(hi), o1 - bf_hi(hi));
     }
     fence_proxy_async();
     __syncthreads();
@@ -406,8 +424,13 @@ __global__ void __launch_bounds__(256, 1)
                 for (int e = 0; e < 16; ++e) v[e] += p[e];
             }
 #pragma unroll
-            for (int e = 0; e < TD_ROWS; ++e)
-                if (e < nb) out[(size_t(b0 + e) * LCA_HEADS + h) * LCA_DV + n] = v[e];
+            for (int e = 0; e < TD_ROWS; ++e) {
+                if constexpr (PAGED) {
+                    if (e < nb && item_len[b0 + e] >= 0)
+                        out16[(size_t(b0 + e) * LCA_HEADS + h) * LCA_DV + n] =
+                            __bfloat16_as_ushort(__float2bfloat16_rn(v[e] + v[e + TD_ROWS]));
+                } else if (e < nb) out[(size_t(b0 + e) * LCA_HEADS + h) * LCA_DV + n] = v[e];
+            }
         }
     }
     tc_fence_before();
