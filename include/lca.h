@@ -409,8 +409,9 @@ int lca_append_paged(const void *rows, int64_t row_pitch, const int64_t *slot_ma
  * selects the kernel (1: single tokens); the result is right whatever it
  * says.  Logits, softmax and sums are fp32; the softmax weights enter the
  * value product as bf16.
- * T < 2^27, n_pages * page_size and max_blocks * page_size < 2^31, and T *
- * max_blocks * page_size / 64 < 2^30 (LCA_ERR_UNSUPPORTED otherwise).
+ * T < 2^27, n_pages * page_size and max_blocks * page_size < 2^31 and, with
+ * max_new = 1, T * max_blocks * page_size / 64 < 2^30 (LCA_ERR_UNSUPPORTED
+ * otherwise).
  * T == 0 is valid.  ws: mla_paged_workspace_bytes(B, T, max_new). */
 size_t mla_paged_workspace_bytes(int B, int64_t T, int max_new);
 int mla_paged_attn(const void *pages, int64_t n_pages, int page_size, const int32_t *block_table, int64_t max_blocks,

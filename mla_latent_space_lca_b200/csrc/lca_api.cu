@@ -24,6 +24,7 @@
 #include "varlen.cuh"
 #include "append.cuh"
 #include "paged.cuh"
+#include "paged_chunk.cuh"
 
 using namespace lca;
 
@@ -71,10 +72,12 @@ int current_device(DeviceInfo **out)
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_REPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_MLA, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(tail_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TD_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(wuv_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PC_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(tables_smem(TB_MAX_BATCH))) == cudaSuccess;
         good &= cudaFuncSetAttribute(condense_kernel<CdShape::kWarps, CdShape::kSlots>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, CdShape::kSmem) == cudaSuccess;
-        good &= cudaFuncSetAttribute(wuv_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(wuv_gemm_kernel<>, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(tail_decode_kernel<>, cudaFuncAttributeMaxDynamicSharedMemorySize, TD_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(condense_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CP_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AP_SMEM_ALLOC) == cudaSuccess;
@@ -193,8 +196,8 @@ struct ProfRec {
 };
 const char *kKernelNames[] = {"",         "prep_summary", "condense",    "attn_decode",      "combine_wuv",
                                "wuv_gemm", "attn_prefill", "condense_prefill", "selftest_wait", "append_token",
-                               "page_tables", "append_paged", "paged_plan"};
-constexpr int kNumKernelIds = 13;
+                               "page_tables", "append_paged", "paged_plan", "paged_chunk", "paged_merge"};
+constexpr int kNumKernelIds = 15;
 bool g_prof_on = false;
 std::vector<ProfRec> g_prof_used;
 std::vector<std::pair<cudaEvent_t, cudaEvent_t>> g_prof_pool;
@@ -503,6 +506,36 @@ PagedWs paged_ws_layout(void *ws, int64_t T)
     return w;
 }
 
+// Workspace of the chunk kernel: the plan, the pieces' partial outputs and o
+// as hi + lo for the W_UV product.
+struct ChunkWs {
+    ChunkPlan plan;
+    float *part_o, *part_ml;
+    uint16_t *o_hl;
+    size_t bytes;
+};
+
+ChunkWs chunk_ws_layout(void *ws, int B, int64_t T)
+{
+    ChunkWs w{};
+    uint8_t *p = static_cast<uint8_t *>(ws);
+    size_t off = 0;
+    const auto take = [&](size_t n) {
+        uint8_t *at = p ? p + off : nullptr;
+        off += align_up(n);
+        return at;
+    };
+    const size_t n = (size_t(B) + 1) * 4;
+    for (int32_t **f : {&w.plan.q0, &w.plan.q1, &w.plan.end, &w.plan.tiles, &w.plan.split, &w.plan.piece_start,
+                        &w.plan.slot_start, &w.plan.merge_start})
+        *f = reinterpret_cast<int32_t *>(take(n));
+    w.part_o = reinterpret_cast<float *>(take(size_t(PC_MAX_SLOTS) * PC_ROWS * LCA_DC * 4));
+    w.part_ml = reinterpret_cast<float *>(take(size_t(PC_MAX_SLOTS) * PC_ROWS * 2 * 4));
+    w.o_hl = reinterpret_cast<uint16_t *>(take(size_t(T) * LCA_HEADS * 2 * LCA_DC * 2));
+    w.bytes = off;
+    return w;
+}
+
 struct PagedCall {
     const void *pages, *q, *w_uv;
     int64_t n_pages, max_blocks, T;
@@ -560,6 +593,59 @@ int run_paged_tokens(DeviceInfo *dev, const PagedCall &c, const PagedWs &w)
                                     (float *)nullptr, rpc, (float *)nullptr, 0, int64_t(0),
                                     (const int32_t *)w.tile_start, static_cast<uint16_t *>(c.out),
                                     (const int32_t *)w.item_len);
+    if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
+    return LCA_OK;
+}
+
+// Query tiles of 8 tokens on pairs of SMs, then W_UV.
+int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
+{
+    int rc = get_encode();
+    if (rc) return rc;
+    ChunkArgs a{};
+    a.plan = w.plan;
+    a.seq_lens = c.seq_lens;
+    a.q_start = c.q_start;
+    a.block_table = c.block_table;
+    a.B = c.B;
+    a.T = int(c.T);
+    a.max_blocks = c.max_blocks;
+    a.n_pages = c.n_pages;
+    a.page_shift = c.shift;
+    a.sl2 = c.scale * 1.4426950408889634f;
+    a.o_hl = w.o_hl;
+    a.part_o = w.part_o;
+    a.part_ml = w.part_ml;
+    const int clusters = std::max(1, dev->sms / 2);
+    CUtensorMap map_q, map_k, map_v, map_a, map_w;
+    const uint64_t rows = uint64_t(c.n_pages) << c.shift, q_rows = uint64_t(c.T) * LCA_HEADS;
+    if ((rc = make_map_rows(&map_q, c.q, q_rows, 1, q_rows, 64)) ||
+        (rc = make_map_pages(&map_k, c.pages, rows, std::min(1 << c.shift, 32), LCA_D / 64)) ||
+        (rc = make_map_pages(&map_v, c.pages, rows, std::min(1 << c.shift, 64), 4)) ||
+        (rc = make_map3(&map_a, w.o_hl, 2 * LCA_DC, LCA_HEADS, uint64_t(c.T), uint64_t(LCA_DC) * 4,
+                        uint64_t(LCA_HEADS) * LCA_DC * 4, 64, 1, 128)) ||
+        (rc = make_map3(&map_w, c.w_uv, LCA_DV, LCA_DC, LCA_HEADS, LCA_DV * 2, LCA_DC * LCA_DV * 2, 64, 64, 1)))
+        return rc;
+    {
+        Launch l(c.st, K_PAGED_PLAN);
+        const cudaError_t e = launch_ex(paged_chunk_plan_kernel, dim3(1), dim3(1024), 0, c.st, true, a, clusters);
+        if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
+    }
+    {
+        Launch l(c.st, K_CHUNK);
+        const cudaError_t e = launch_ex(paged_chunk_kernel, dim3(2 * clusters), dim3(PC_THREADS), PC_SMEM_ALLOC, c.st,
+                                        true, map_q, map_k, map_v, a);
+        if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
+    }
+    {
+        Launch l(c.st, K_MERGE);
+        const cudaError_t e = launch_ex(paged_merge_kernel, dim3(2 * dev->sms), dim3(MG_THREADS), 0, c.st, true, a);
+        if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
+    }
+    Launch l(c.st, K_GEMM);
+    const cudaError_t e = launch_ex(wuv_gemm_kernel<true>, dim3(unsigned((c.T + 127) / 128), LCA_HEADS), dim3(128),
+                                    GM_SMEM_ALLOC, c.st, true, map_a, map_w, (float *)nullptr, c.T,
+                                    static_cast<uint16_t *>(c.out), c.q_start, c.B);
     if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     return LCA_OK;
 }
@@ -1009,9 +1095,10 @@ int lca_prefill_block(const void *cache, const void *q, const void *w_uv, int B,
                                     uint64_t(LCA_HEADS) * LCA_DC * 2, 64, 1, 128)))
                     return rc;
                 Launch l(st, K_GEMM);
-                const cudaError_t e = launch_ex(wuv_gemm_kernel, dim3(unsigned((R + 127) / 128), LCA_HEADS),
+                const cudaError_t e = launch_ex(wuv_gemm_kernel<>, dim3(unsigned((R + 127) / 128), LCA_HEADS),
                                                 dim3(128), GM_SMEM_ALLOC, st, false, map_a, map_w,
-                                                out + row_out * LCA_HEADS * LCA_DV, R);
+                                                out + row_out * LCA_HEADS * LCA_DV, R, (uint16_t *)nullptr,
+                                                (const int32_t *)nullptr, 0);
                 if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
             }
         }
@@ -1115,7 +1202,7 @@ int lca_append_paged(const void *rows, int64_t row_pitch, const int64_t *slot_ma
 size_t mla_paged_workspace_bytes(int B, int64_t T, int max_new)
 {
     if (B < 1 || T < 1 || max_new < 1 || T >= (int64_t(1) << 27)) return 0;
-    return paged_ws_layout(nullptr, T).bytes;
+    return max_new == 1 ? paged_ws_layout(nullptr, T).bytes : chunk_ws_layout(nullptr, B, T).bytes;
 }
 
 int mla_paged_attn(const void *pages, int64_t n_pages, int page_size, const int32_t *block_table, int64_t max_blocks,
@@ -1129,20 +1216,23 @@ int mla_paged_attn(const void *pages, int64_t n_pages, int page_size, const int3
     if (shift < 0 || n_pages > (int64_t(0x7fffffff) >> shift) || max_blocks > (int64_t(0x7fffffff) >> shift) ||
         T >= (int64_t(1) << 27))
         return LCA_ERR_UNSUPPORTED;
-    // tile offsets are int32: every token's tiles together must stay below 2^30
-    if (T * (((max_blocks << shift) + AT_TILE - 1) / AT_TILE) >= (int64_t(1) << 30)) return LCA_ERR_UNSUPPORTED;
+    // single tokens: tile offsets are int32, so all tokens' tiles together must stay below 2^30
+    if (max_new == 1 && T * (((max_blocks << shift) + AT_TILE - 1) / AT_TILE) >= (int64_t(1) << 30))
+        return LCA_ERR_UNSUPPORTED;
     if (!aligned16(pages) || !aligned16(q) || !aligned16(w_uv) || !aligned16(out)) return LCA_ERR_MISALIGNED;
     for (const int32_t *p : {block_table, seq_lens, q_start})
         if (reinterpret_cast<uintptr_t>(p) & 3u) return LCA_ERR_MISALIGNED;
     if (T == 0) return LCA_OK;
-    const PagedWs w = paged_ws_layout(ws, T);
-    int rc = check_ws(ws, ws_bytes, w.bytes);
+    int rc = check_ws(ws, ws_bytes, mla_paged_workspace_bytes(B, T, max_new));
     if (rc) return rc;
     DeviceInfo *dev = nullptr;
     if ((rc = current_device(&dev))) return rc;
     const PagedCall c{pages, q, w_uv, n_pages, max_blocks, T, block_table, seq_lens, q_start, B, shift, scale, out,
                       static_cast<cudaStream_t>(stream)};
-    return run_paged_tokens(dev, c, w);
+    // one token a sequence: 16 query rows against a stream of rows, a memory-
+    // bound split-L decode.  More: the tiles of 8 tokens read a sequence's
+    // rows once for all of them.
+    return max_new == 1 ? run_paged_tokens(dev, c, paged_ws_layout(ws, T)) : run_paged_chunks(dev, c, chunk_ws_layout(ws, B, T));
 }
 
 int lca_selftest_wait_timeout(void *stream)
