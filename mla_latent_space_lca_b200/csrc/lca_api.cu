@@ -525,12 +525,12 @@ ChunkWs chunk_ws_layout(void *ws, int B, int64_t T)
         off += align_up(n);
         return at;
     };
-    const size_t n = (size_t(B) + 1) * 4;
-    for (int32_t **f : {&w.plan.q0, &w.plan.q1, &w.plan.end, &w.plan.tiles, &w.plan.split, &w.plan.piece_start,
-                        &w.plan.slot_start, &w.plan.merge_start})
-        *f = reinterpret_cast<int32_t *>(take(n));
-    w.part_o = reinterpret_cast<float *>(take(size_t(PC_MAX_SLOTS) * PC_ROWS * LCA_DC * 4));
-    w.part_ml = reinterpret_cast<float *>(take(size_t(PC_MAX_SLOTS) * PC_ROWS * 2 * 4));
+    for (int32_t **f : {&w.plan.q0, &w.plan.q1, &w.plan.tile0}) *f = reinterpret_cast<int32_t *>(take(size_t(B) * 4));
+    w.plan.tile = reinterpret_cast<ChunkTile *>(take((size_t(T) / PC_TOKENS + size_t(B) + 1) * sizeof(ChunkTile)));
+    w.plan.first = reinterpret_cast<int32_t *>(take(PC_MAX_CLUSTERS * 4));
+    w.plan.nq = reinterpret_cast<int32_t *>(take(4));
+    w.part_o = reinterpret_cast<float *>(take(size_t(2 * PC_MAX_CLUSTERS) * PC_ROWS * LCA_DC * 4));
+    w.part_ml = reinterpret_cast<float *>(take(size_t(2 * PC_MAX_CLUSTERS) * PC_ROWS * 2 * 4));
     w.o_hl = reinterpret_cast<uint16_t *>(take(size_t(T) * LCA_HEADS * 2 * LCA_DC * 2));
     w.bytes = off;
     return w;
@@ -616,12 +616,12 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
     a.o_hl = w.o_hl;
     a.part_o = w.part_o;
     a.part_ml = w.part_ml;
-    const int clusters = std::max(1, dev->sms / 2);
+    const int clusters = std::min(std::max(1, dev->sms / 2), PC_MAX_CLUSTERS);
     CUtensorMap map_q, map_k, map_v, map_a, map_w;
     const uint64_t rows = uint64_t(c.n_pages) << c.shift, q_rows = uint64_t(c.T) * LCA_HEADS;
     if ((rc = make_map_rows(&map_q, c.q, q_rows, 1, q_rows, 64)) ||
-        (rc = make_map_pages(&map_k, c.pages, rows, std::min(1 << c.shift, 32), LCA_D / 64)) ||
-        (rc = make_map_pages(&map_v, c.pages, rows, std::min(1 << c.shift, 64), 4)) ||
+        (rc = make_map_pages(&map_k, c.pages, rows, std::min(1 << c.shift, 64), 1)) ||
+        (rc = make_map_pages(&map_v, c.pages, rows, 16, 4)) ||
         (rc = make_map3(&map_a, w.o_hl, 2 * LCA_DC, LCA_HEADS, uint64_t(c.T), uint64_t(LCA_DC) * 4,
                         uint64_t(LCA_HEADS) * LCA_DC * 4, 64, 1, 128)) ||
         (rc = make_map3(&map_w, c.w_uv, LCA_DV, LCA_DC, LCA_HEADS, LCA_DV * 2, LCA_DC * LCA_DV * 2, 64, 64, 1)))
@@ -637,9 +637,10 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
                                         true, map_q, map_k, map_v, a);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
-    {
+    if (clusters > 1) {
         Launch l(c.st, K_MERGE);
-        const cudaError_t e = launch_ex(paged_merge_kernel, dim3(2 * dev->sms), dim3(MG_THREADS), 0, c.st, true, a);
+        const cudaError_t e = launch_ex(paged_merge_kernel, dim3(PC_ROWS * 32 / MG_THREADS, clusters - 1),
+                                        dim3(MG_THREADS), 0, c.st, true, a, clusters);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     Launch l(c.st, K_GEMM);
