@@ -12,8 +12,9 @@
 // Neither Q nor P nor the accumulators cross between the SMs.  The accumulator
 // of 64 x 512 fp32 takes 256 columns of tensor memory, spread over all 128
 // lanes (lanes 0-63 hold rows 0-63 and the columns of the first half of N,
-// lanes 64-127 the same rows and the second half), so a softmax thread owns
-// half a row: 64 of the 128 logits, 256 of the 512 outputs.
+// lanes 64-127 the same rows and the second half); two softmax threads share a
+// lane's columns, so each owns a quarter of a row: 32 of the 128 logits, 128
+// of the 512 outputs.
 //
 // A tile is fetched in slots of 8 KB: nine for S ([64 rows][64 columns], this
 // CTA's rows) and eight for PV ([16 rows][256 columns], this CTA's columns),
@@ -38,17 +39,18 @@ constexpr int PC_SLOTS = PC_KRING + PC_VRING;
 constexpr int PC_P = 2 * 8192;                   // P [64 x 128] bf16, two [64 x 64] blocks
 constexpr int PC_OFF_P = PC_Q;
 constexpr int PC_OFF_RING = PC_OFF_P + 2 * PC_P;
-constexpr int PC_OFF_X = PC_OFF_RING + PC_SLOTS * PC_SLOT;   // [2][128] maxima, [128] sums
-constexpr int PC_OFF_BAR = PC_OFF_X + 3 * 128 * 4;
+constexpr int PC_OFF_X = PC_OFF_RING + PC_SLOTS * PC_SLOT;   // [2][256] row maxima or sums
+constexpr int PC_OFF_BAR = PC_OFF_X + 2 * 256 * 4;
 constexpr int PC_BARS = 2 * PC_SLOTS + 15;
 constexpr int PC_OFF_MISC = PC_OFF_BAR + 8 * PC_BARS;
 constexpr int PC_SMEM = PC_OFF_MISC + 16;
-constexpr int PC_SMEM_ALLOC = PC_SMEM + 1024;
+constexpr int PC_SMEM_ALLOC = PC_SMEM;   // no room to align it: the kernel checks that it starts at 1024 bytes
 static_assert(PC_SMEM_ALLOC <= 227 * 1024, "one CTA per SM");
 constexpr uint32_t PC_TM_O = 0, PC_TM_S = 256;   // O 256 columns, S two buffers of 64
-constexpr int PC_PRODUCERS = 2;                  // warps 4, 5 for S, 6, 7 for PV
-constexpr int PC_WARP_S = 8, PC_WARP_PV = 9;     // MMA issue (CTA 0)
-constexpr int PC_THREADS = 32 * 10;
+constexpr int PC_SOFTMAX = 8;                    // warps 0 .. 7
+constexpr int PC_PRODUCERS = 2;                  // warps 8, 9 for S, 10, 11 for PV
+constexpr int PC_WARP_S = 12, PC_WARP_PV = 13;   // MMA issue (CTA 0)
+constexpr int PC_THREADS = 32 * 14;
 constexpr int PC_MAX_CLUSTERS = 80;              // partial outputs: two per cluster
 constexpr int PC_OVER = 2;                       // cost of a piece beyond its tiles, in tiles
 
@@ -228,37 +230,67 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// mbar_wait by a whole warp: the same answer in every lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, int site)
-{
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const uint64_t t0 = globaltimer();
-    for (uint32_t it = 1;; ++it) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((it & 63u) == 0) {
-            if (__any_sync(0xffffffffu, *abort != 0)) return false;
-            if (__any_sync(0xffffffffu, globaltimer() - t0 > kWaitLimitNs)) {
-                report_timeout(K_CHUNK, site);
-                *abort = 1;
-                return false;
-            }
-        }
-    }
-}
-
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // One lane of the (converged) warp, the same each time.  MMAs issued under it
-// keep their descriptors in uniform registers: 26 cycles each, against 80
-// under `lane == 0`.
+// take 26 to 37 cycles each as long as little else is under it (80 under `lane
+// == 0`, and where whole loops run in one lane): the loops and the waits stay
+// with the whole warp.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t p;
     asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// mbar_wait by one lane for the whole warp (32 lanes that poll a barrier take
+// the shared-memory pipe from everybody else); the same answer in every lane.
+// The loop stands apart: with it inline at every wait and the loops over slots
+// unrolled, the warps' different roles kept evicting each other's instructions
+// (half of all stall cycles; 2.0 times the run time).
+__device__ __noinline__ bool warp_wait_more(uint32_t bar, uint32_t parity, volatile int *abort, int site)
+{
+    bool ok = false;
+    if (elect_one()) ok = mbar_wait(bar, parity, abort, K_CHUNK, site);
+    return __any_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, int site)
+{
+    bool ok = false;
+    if (elect_one()) ok = mbar_try_wait(bar, parity);
+    ok = __any_sync(0xffffffffu, ok) || warp_wait_more(bar, parity, abort, site);
+    __syncwarp();
+    return ok;
+}
+
+// A place in a ring of N slots: its slot, and the parity of its use.
+template <int N>
+struct RingPlace {
+    uint32_t slot = 0, par = 0;
+    __device__ __forceinline__ void operator++()
+    {
+        if (++slot == N) {
+            slot = 0;
+            par ^= 1;
+        }
+    }
+};
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void mma2_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -351,27 +383,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const ChunkArgs a)
 {
-    extern __shared__ uint8_t pc_smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(pc_smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
+    if (sbase & 1023u) {   // the same in every CTA
+        report_timeout(K_CHUNK, 0);
+        return;
+    }
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     uint32_t cta;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(cta));
 
     auto BAR = [&](int i) -> uint32_t { return sbase + PC_OFF_BAR + 8 * i; };
     // CTA 0's: both CTAs' copies into a slot have landed / its own: the slot is free.
-    // Slot of the x-th use of a ring, and the parity of that use.
-    auto kslot = [&](uint32_t x) { return x % PC_KRING; };
-    auto vslot = [&](uint32_t x) { return x % PC_VRING; };
-    auto kpar = [&](uint32_t x) { return (x / PC_KRING) & 1; };
-    auto vpar = [&](uint32_t x) { return (x / PC_VRING) & 1; };
-    auto kfull = [&](uint32_t x) { return BAR(int(kslot(x))); };
-    auto kempty = [&](uint32_t x) { return BAR(PC_KRING + int(kslot(x))); };
-    auto vfull = [&](uint32_t x) { return BAR(2 * PC_KRING + int(vslot(x))); };
-    auto vempty = [&](uint32_t x) { return BAR(2 * PC_KRING + PC_VRING + int(vslot(x))); };
-    auto kaddr = [&](uint32_t x) { return sbase + PC_OFF_RING + kslot(x) * PC_SLOT; };
-    auto vaddr = [&](uint32_t x) { return sbase + PC_OFF_RING + (PC_KRING + vslot(x)) * PC_SLOT; };
+    auto kfull = [&](uint32_t slot) { return BAR(int(slot)); };
+    auto kempty = [&](uint32_t slot) { return BAR(PC_KRING + int(slot)); };
+    auto vfull = [&](uint32_t slot) { return BAR(2 * PC_KRING + int(slot)); };
+    auto vempty = [&](uint32_t slot) { return BAR(2 * PC_KRING + PC_VRING + int(slot)); };
+    auto kaddr = [&](uint32_t slot) { return sbase + PC_OFF_RING + slot * PC_SLOT; };
+    auto vaddr = [&](uint32_t slot) { return sbase + PC_OFF_RING + (PC_KRING + slot) * PC_SLOT; };
     constexpr int B0 = 2 * PC_SLOTS;
     const uint32_t qfull = BAR(B0);
     // MMAs done, in both CTAs: S(n), PV(n)
@@ -383,13 +412,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     const uint32_t oread = BAR(B0 + 9);
     const uint32_t vready = BAR(B0 + 10);   // in both CTAs: an edge tile's PV slots have landed
     const uint32_t drain_s = BAR(B0 + 11), drain_pv = BAR(B0 + 12);
-    // the two softmax warps that share their rows have written what they exchange
+    // the four softmax warps that share their rows have written what they exchange
     const uint32_t xchg = BAR(B0 + 13 + (warp & 1));
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + PC_OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + PC_OFF_MISC + 4);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < PC_BARS; ++i) mbar_init(BAR(i), i < B0 + 5 ? 1 : i <= B0 + 9 ? 8 : i <= B0 + 12 ? 1 : 2);
+        for (int i = 0; i < PC_BARS; ++i) mbar_init(BAR(i), i < B0 + 5 ? 1 : i <= B0 + 9 ? 2 * PC_SOFTMAX : i <= B0 + 12 ? 1 : PC_SOFTMAX / 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -411,13 +440,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     ChunkRange range(a.plan, int(blockIdx.x >> 1), int(gridDim.x >> 1));
     ChunkPiece w;
 
-    if (warp >= 4 && warp < 4 + 2 * PC_PRODUCERS) {
+    if (warp >= PC_SOFTMAX && warp < PC_SOFTMAX + 2 * PC_PRODUCERS) {
         // ------------------------------------------------------------ producers
-        // Warps 4 and 5 bring S's slots in turn, warps 6 and 7 PV's (one warp
-        // takes ~320 cycles a slot, the MMAs use one of either ring every 250
-        // to 280).
+        // Two warps bring S's slots in turn, two PV's: one takes about 200
+        // cycles a slot and 50 more for each further page in it, the MMAs use
+        // a slot of either ring every 250 to 280.
         const uint32_t p = uint32_t(warp) & 1;
-        const bool is_k = warp < 4 + PC_PRODUCERS;
+        const bool is_k = warp < PC_SOFTMAX + PC_PRODUCERS;
         const int k_shift = min(a.page_shift, 6);
         const int64_t no_page = a.n_pages << (a.page_shift - 3);   // beyond the map: zeros
         const int64_t in_page = (int64_t(1) << a.page_shift) - 1;
@@ -425,7 +454,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             prefetch_tensormap(is_k ? &map_k : &map_v);
             if (is_k && p == 0) prefetch_tensormap(&map_q);
         }
-        uint32_t n = 0, x = 0;   // tiles, ring uses
+        const int ring = is_k ? PC_KRING : PC_VRING;
+        const uint32_t first_full = is_k ? kfull(0) : vfull(0), first_empty = is_k ? kempty(0) : vempty(0);
+        const uint32_t first_slot = is_k ? kaddr(0) : vaddr(0);
+        // copies into a slot: the pages in a K slot's 64 rows; a V slot's 16 rows lie in one
+        const int copies = is_k ? 64 >> k_shift : 1;
+        const CUtensorMap *map = is_k ? &map_k : &map_v;
+        uint32_t n = 0, x = 0, slot = 0, par = 0;   // tiles, ring uses; x's slot and its parity
         bool ok = true;
         while (ok && range.next(a.plan, w)) {
             if (w.n() == 0) continue;
@@ -444,45 +479,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             win.open(a.block_table + size_t(w.t.b) * size_t(a.max_blocks), row0 >> a.page_shift, a.max_blocks, a.n_pages,
                      lane);
             for (int i = 0; i < w.n() && ok; ++i, ++n, row0 += PC_TILE) {
-                const uint32_t end = x + uint32_t(is_k ? PC_KS : w.v_slots(i, max_rows));
-                for (int part = 0; x < end; ++x, ++part) {
-                    if ((x & 1) != p) continue;
-                    ok = is_k ? warp_wait(kempty(x), kpar(x) ^ 1, abort_flag, 2)
-                              : warp_wait(vempty(x), vpar(x) ^ 1, abort_flag, 3);
-                    if (!ok) break;
-                    const uint32_t full = is_k ? kfull(x) : vfull(x), bar = map_to_cta(full, 0);
-                    if (cta == 0 && elect_one()) mbar_expect_tx(full, 2 * PC_SLOT);
-                    if (is_k) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (c < (64 >> k_shift)) {
-                                const int64_t r = row0 + (int64_t(c) << k_shift);
-                                const int32_t page = win.at(r >> a.page_shift, lane);
-                                const int64_t group =
-                                    page >= 0 ? ((int64_t(page) << a.page_shift) + (r & in_page)) >> 3 : no_page;
-                                if (elect_one())
-                                    tma_load_4d_pair(kaddr(x) + ((c << k_shift) >> 3) * 1024, &map_k, bar, 0, 0, part,
-                                                     int(group));
-                            }
+                const int parts = is_k ? PC_KS : w.v_slots(i, max_rows);
+#pragma unroll 1
+                for (int part = 0; part < parts; ++part, ++x) {
+                    if ((x & 1) == p) {
+                        if (!(ok = warp_wait(first_empty + 8 * slot, par ^ 1, abort_flag, 2))) break;
+                        const uint32_t bar = map_to_cta(first_full + 8 * slot, 0), dst = first_slot + slot * PC_SLOT;
+                        if (cta == 0 && elect_one()) mbar_expect_tx(first_full + 8 * slot, 2 * PC_SLOT);
+#pragma unroll 1
+                        for (int c = 0; c < copies; ++c) {
+                            const int64_t r = row0 + (is_k ? int64_t(c) << k_shift : 16 * part);
+                            const int32_t page = win.at(r >> a.page_shift, lane);
+                            const int64_t group =
+                                page >= 0 ? ((int64_t(page) << a.page_shift) + (r & in_page)) >> 3 : no_page;
+                            if (elect_one())
+                                tma_load_4d_pair(dst + ((c << k_shift) >> 3) * 1024, map, bar, 0, 0,
+                                                 is_k ? part : 4 * int(cta), int(group));
                         }
-                    } else {
-                        const int64_t r = row0 + 16 * part;
-                        const int32_t page = win.at(r >> a.page_shift, lane);
-                        const int64_t group = page >= 0 ? ((int64_t(page) << a.page_shift) + (r & in_page)) >> 3 : no_page;
-                        if (elect_one()) tma_load_4d_pair(vaddr(x), &map_v, bar, 0, 0, 4 * int(cta), int(group));
                     }
-                    __syncwarp();
+                    if (++slot == uint32_t(ring)) {
+                        slot = 0;
+                        par ^= 1;
+                    }
                 }
             }
         }
-        // no copy left in flight, and every commit that arrives at this CTA has
-        const uint32_t ring = is_k ? PC_KRING : PC_VRING;
-        for (uint32_t y = x > ring ? x - ring : 0; y < x; ++y) {
-            if (!ok || (y & 1) != p) continue;
-            if (cta == 0)
-                ok = is_k ? warp_wait(kfull(y), kpar(y), abort_flag, 4) : warp_wait(vfull(y), vpar(y), abort_flag, 5);
-            ok = ok && (is_k ? warp_wait(kempty(y), kpar(y), abort_flag, 6)
-                             : warp_wait(vempty(y), vpar(y), abort_flag, 7));
+        // no copy left in flight, and every commit that arrives at this CTA
+        // has: this warp's among the ring's last uses, backwards
+#pragma unroll 1
+        for (int back = 0; back < ring && x > 0 && ok; ++back) {
+            --x;
+            if (slot == 0) {
+                slot = uint32_t(ring);
+                par ^= 1;
+            }
+            --slot;
+            if ((x & 1) != p) continue;
+            if (cta == 0) ok = warp_wait(first_full + 8 * slot, par, abort_flag, 4);
+            ok = ok && warp_wait(first_empty + 8 * slot, par, abort_flag, 6);
         }
         if (!ok) {   // given up: copies may still be under way
             const uint64_t t0 = globaltimer();
@@ -491,8 +525,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     } else if (warp == PC_WARP_S && cta == 0) {
         // ------------------------------------------------------------ S = Q . tile^T for the pair
         constexpr uint32_t IDESC_S = idesc_bf16(PC_ROWS, PC_TILE, 0, 0);
-        uint32_t n = 0, x = 0, pieces = 0;
-        bool ok = true;
+        RingPlace<PC_KRING> at;
+        uint32_t n = 0, pieces = 0;
+        bool ok = true, there = false;   // there: the slot has been seen to have landed
         while (ok && range.next(a.plan, w)) {
             const int m = __shfl_sync(0xffffffffu, w.n(), 0);
             if (m == 0) continue;
@@ -500,35 +535,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             for (int i = 0; i < m && ok; ++i, ++n) {
                 if (!(ok = warp_wait(sread(n), ((n >> 1) & 1) ^ 1, abort_flag, 9))) break;
                 const uint32_t d = tmem + PC_TM_S + 64 * (n & 1);
-#pragma unroll
-                for (int c = 0; c < PC_KS; ++c, ++x) {
-                    if (!(ok = warp_wait(kfull(x), kpar(x), abort_flag, 10))) break;
+#pragma unroll 1
+                for (int c = 0; c < PC_KS; ++c) {
+                    if (!there && !(ok = warp_wait(kfull(at.slot), at.par, abort_flag, 10))) break;
                     tc_fence_after();
+                    const RingPlace<PC_KRING> now = at;
+                    ++at;
+                    bool next = false;
                     if (elect_one()) {
-                        const uint32_t kst = kaddr(x);
+                        next = mbar_test(kfull(at.slot), at.par);   // its ~100 cycles pass under the MMAs
+                        const uint64_t qd = sdesc_sw128(sbase + c * 8192, 16, 1024);
+                        const uint64_t kd = sdesc_sw128(kaddr(now.slot), 16, 1024);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma2_ss(d, sdesc_sw128(sbase + c * 8192 + ks * 32, 16, 1024),
-                                    sdesc_sw128(kst + ks * 32, 16, 1024), IDESC_S, c + ks ? 1u : 0u);
-                        tc_commit_pair(kempty(x));
+                        for (int ks = 0; ks < 4; ++ks) mma2_ss(d, qd + 2 * ks, kd + 2 * ks, IDESC_S, c + ks ? 1u : 0u);
+                        tc_commit_pair(kempty(now.slot));
                         if (c == PC_KS - 1) tc_commit_pair(sdone(n));
                     }
-                    __syncwarp();
+                    there = __any_sync(0xffffffffu, next);
                 }
             }
             ++pieces;
         }
         // the other CTA's last arrivals are in, and no MMA is left in flight
-        if (ok && n > 0) ok = warp_wait(sread(n - 1), ((n - 1) >> 1) & 1, abort_flag, 20);
+        if (ok && n > 0) warp_wait(sread(n - 1), ((n - 1) >> 1) & 1, abort_flag, 20);
         if (elect_one())
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain_s)
                          : "memory");
         __syncwarp();
-        mbar_wait(drain_s, 0, nullptr, K_CHUNK, 8);
+        warp_wait(drain_s, 0, abort_flag, 21);
+        __syncwarp();
     } else if (warp == PC_WARP_PV && cta == 0) {
         // ------------------------------------------------------------ O += P . tile for the pair
         constexpr uint32_t IDESC_PV = idesc_bf16(PC_ROWS, 256, 0, 1);
-        uint32_t n = 0, x = 0, pieces = 0;
+        RingPlace<PC_VRING> at;
+        uint32_t n = 0, pieces = 0;
         bool ok = true;
         while (ok && range.next(a.plan, w)) {
             const int m = __shfl_sync(0xffffffffu, w.n(), 0);
@@ -538,58 +578,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 const int nvs = __shfl_sync(0xffffffffu, w.v_slots(i, max_rows), 0);
                 if (int64_t(w.k0 + i + 1) * PC_TILE > nv_all) {
                     // an edge tile (see the softmax): its rows have landed
-                    for (int v = 0; v < nvs && ok; ++v)
-                        ok = warp_wait(vfull(x + v), vpar(x + v), abort_flag, 11);
+                    RingPlace<PC_VRING> x = at;
+#pragma unroll 1
+                    for (int v = 0; v < nvs && ok; ++v, ++x) ok = warp_wait(vfull(x.slot), x.par, abort_flag, 11);
                     if (!ok) break;
                     if (lane < 2) mbar_arrive_pair(map_to_cta(vready, lane));
+                    __syncwarp();
                 }
                 if (i == 0 && !(ok = warp_wait(oread, (pieces & 1) ^ 1, abort_flag, 12))) break;
                 if (!(ok = warp_wait(pfull(n), (n >> 1) & 1, abort_flag, 13))) break;
+                bool there = false;
                 const uint32_t pst = sbase + PC_OFF_P + (n & 1) * PC_P;
-#pragma unroll
-                for (int v = 0; v < PC_VS; ++v) {
-                    if (v >= nvs) break;
-                    if (!(ok = warp_wait(vfull(x + v), vpar(x + v), abort_flag, 14))) break;
+#pragma unroll 1
+                for (int v = 0; v < nvs; ++v) {
+                    if (!there && !(ok = warp_wait(vfull(at.slot), at.par, abort_flag, 14))) break;
                     tc_fence_after();
+                    const RingPlace<PC_VRING> now = at;
+                    ++at;
+                    bool next = false;
                     if (elect_one()) {
-                        const uint32_t vst = vaddr(x + v);
+                        next = mbar_test(vfull(at.slot), at.par);
+                        const uint64_t pd = sdesc_sw128(pst + (v >> 2) * 8192 + (v & 3) * 32, 16, 1024);
+                        const uint64_t vd = sdesc_sw128(vaddr(now.slot), 1024, 4096);
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
-                            mma2_ss(tmem + PC_TM_O + 128 * j,
-                                    sdesc_sw128(pst + (v >> 2) * 8192 + (v & 3) * 32, 16, 1024),
-                                    sdesc_sw128(vst + j * 2048, 1024, 4096), IDESC_PV, (i > 0 || v > 0) ? 1u : 0u);
-                        tc_commit_pair(vempty(x + v));
+                            mma2_ss(tmem + PC_TM_O + 128 * j, pd, vd + 128 * j, IDESC_PV, (i > 0 || v > 0) ? 1u : 0u);
+                        tc_commit_pair(vempty(now.slot));
                         if (v == nvs - 1) tc_commit_pair(vdone(n));
                     }
-                    __syncwarp();
+                    there = __any_sync(0xffffffffu, next);
                 }
-                x += uint32_t(nvs);
             }
             ++pieces;
         }
-        if (ok && pieces > 0) ok = warp_wait(oread, (pieces - 1) & 1, abort_flag, 21);
+        if (ok && pieces > 0) warp_wait(oread, (pieces - 1) & 1, abort_flag, 22);
         if (elect_one())
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drain_pv)
                          : "memory");
         __syncwarp();
-        mbar_wait(drain_pv, 0, nullptr, K_CHUNK, 13);
-    } else if (warp < 4) {
+        warp_wait(drain_pv, 0, abort_flag, 24);
+        __syncwarp();
+    } else if (warp < PC_SOFTMAX) {
         // ------------------------------------------------------------ softmax and epilogue
-        const int row = (32 * warp + lane) & 63, half = warp >> 1;
-        const uint32_t lane_base = uint32_t(32 * warp) << 16;
-        float *xm = reinterpret_cast<float *>(smem + PC_OFF_X);
-        const int mine = 32 * warp + lane, other = mine ^ 64;
+        // half: which 64 of the tile's rows and 256 of o's columns this lane of
+        // tensor memory holds; quad: which half of those is this warp's
+        const int lane4 = 32 * (warp & 3) + lane, row = lane4 & 63, half = lane4 >> 6, quad = warp >> 2;
+        const uint32_t lane_base = uint32_t(32 * (warp & 3)) << 16;
+        float *xm = reinterpret_cast<float *>(smem + PC_OFF_X);   // [2][quad][half][row]
+        const int mine = 128 * quad + lane4;
         const int tok = 4 * int(cta) + (row >> 4), head = row & 15;
         const uint32_t peer_sread = map_to_cta(sread(0), 0), peer_pfull = map_to_cta(pfull(0), 0);
         const uint32_t peer_oread = map_to_cta(oread, 0);
         const int sub_shift = min(a.page_shift, 7), subs = PC_TILE >> sub_shift;
         uint32_t n = 0, x0 = 0, edges = 0, swaps = 0;   // x0: first use of PV's ring
         bool ok = true;
-        // warps w and w + 2 share their rows: what either wrote is there for the other
-        const auto exchanged = [&]() {
+        // Puts this thread's value beside those of the other three that share
+        // its row (warps w + 2, w + 4, w + 6 modulo 8).  Two buffers in turn: who
+        // writes one has seen everybody past the exchange that used it last.
+        const auto exchange = [&](float v) {
+            xm[(swaps & 1) * 256 + mine] = v;
             __syncwarp();
             if (lane == 0) mbar_arrive(xchg);
             return warp_wait(xchg, swaps++ & 1, abort_flag, 19);
+        };
+        const auto of_row = [&](auto f) {
+            const float *v = xm + ((swaps & 1) ^ 1) * 256 + row;
+            return f(f(v[0], v[64]), f(v[128], v[192]));
         };
         while (ok && range.next(a.plan, w)) {
             const int32_t t = w.t.t0 + tok;
@@ -607,15 +661,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 const int64_t row0 = int64_t(w.k0 + i) * PC_TILE;
                 // which of the tile's pages are there
                 uint32_t pages = 0;
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (c < subs && win.at((row0 + (int64_t(c) << sub_shift)) >> a.page_shift, lane) >= 0)
-                        pages |= 1u << c;
+#pragma unroll 1
+                for (int c = 0; c < subs; ++c)
+                    if (win.at((row0 + (int64_t(c) << sub_shift)) >> a.page_shift, lane) >= 0) pages |= 1u << c;
                 const bool whole = pages == (1u << subs) - 1u;
                 if (!(ok = warp_wait(sdone(n), (n >> 1) & 1, abort_flag, 15))) break;
                 tc_fence_after();
-                float s[64];
-                tmem_ld64(tmem + lane_base + PC_TM_S + 64 * (n & 1), s);
+                float s[32];
+                tmem_ld32(tmem + lane_base + PC_TM_S + 64 * (n & 1) + 32 * quad, s);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(peer_sread + 8 * (n & 1));
@@ -629,51 +682,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     // clear what is not finite in this CTA's columns of them
                     // (a token that does attend the row has the NaN in its
                     // weight already).
-                    uint32_t odd[2] = {0, 0};
+                    uint32_t odd = 0;
 #pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (!(fabsf(s[x]) <= 3.4e38f)) odd[x >> 5] |= 1u << (x & 31);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) odd[h] = __reduce_or_sync(0xffffffffu, odd[h]);
+                    for (int x = 0; x < 32; ++x)
+                        if (!(fabsf(s[x]) <= 3.4e38f)) odd |= 1u << x;
+                    odd = __reduce_or_sync(0xffffffffu, odd);
                     if (!(ok = warp_wait(vready, edges & 1, abort_flag, 16))) break;
-                    if (odd[0] | odd[1]) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            while (odd[h]) {
-                                const int r = 64 * half + 32 * h + __ffs(int(odd[h])) - 1;
-                                odd[h] &= odd[h] - 1;
-                                if ((r >> 4) >= nvs) break;
-                                uint4 *p = reinterpret_cast<uint4 *>(
-                                    smem + (vaddr(x0 + (r >> 4)) - sbase) + ((r >> 3) & 1) * 4096 + (lane >> 3) * 1024 +
-                                    (r & 7) * 128 + (lane & 7) * 16);
-                                const uint4 v = *p;
-                                bool bad = false;
-                                for (uint32_t e : {v.x, v.y, v.z, v.w})
-                                    bad |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
-                                if (__any_sync(0xffffffffu, bad)) *p = make_uint4(0u, 0u, 0u, 0u);
-                            }
+                    while (odd) {
+                        const int r = 64 * half + 32 * quad + __ffs(int(odd)) - 1;
+                        odd &= odd - 1;
+                        if ((r >> 4) >= nvs) break;
+                        uint4 *p = reinterpret_cast<uint4 *>(smem + (vaddr((x0 + (r >> 4)) % PC_VRING) - sbase) + ((r >> 3) & 1) * 4096 +
+                                                             (lane >> 3) * 1024 + (r & 7) * 128 + (lane & 7) * 16);
+                        const uint4 v = *p;
+                        bool bad = false;
+                        for (uint32_t e : {v.x, v.y, v.z, v.w})
+                            bad |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
+                        if (__any_sync(0xffffffffu, bad)) *p = make_uint4(0u, 0u, 0u, 0u);
                     }
                     ++edges;
                 }
-                if (edge || !live) {
-                    const int64_t left = int64_t(nv) - row0 - 64 * half;
-                    const int lim = left < 0 ? 0 : int(min64(left, 64));
+                if (edge || !live || !whole) {
+                    const int64_t left = int64_t(nv) - row0 - 64 * half - 32 * quad;
+                    uint32_t in = left <= 0 ? 0u : left >= 32 ? ~0u : (1u << int(left)) - 1u;
 #pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (x >= lim) s[x] = -INFINITY;
-                }
-                if (!whole) {
+                    for (int c = 0; c < 2; ++c)   // 16 rows lie in one page
+                        if (!((pages >> ((64 * half + 32 * quad + 16 * c) >> sub_shift)) & 1u)) in &= ~(0xffffu << (16 * c));
 #pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (!((pages >> ((64 * half + x) >> sub_shift)) & 1u)) s[x] = -INFINITY;
+                    for (int x = 0; x < 32; ++x)
+                        if (!((in >> x) & 1u)) s[x] = -INFINITY;
                 }
                 float tm[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int x = 4; x < 64; ++x) tm[x & 3] = fmaxf(tm[x & 3], s[x]);
+                for (int x = 4; x < 32; ++x) tm[x & 3] = fmaxf(tm[x & 3], s[x]);
                 float tmax = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3]));
-                xm[(n & 1) * 128 + mine] = tmax;
-                if (!(ok = exchanged())) break;
-                tmax = fmaxf(tmax, xm[(n & 1) * 128 + other]) * a.sl2;
+                if (!(ok = exchange(tmax))) break;
+                tmax = of_row([](float u, float v) { return fmaxf(u, v); }) * a.sl2;
                 float f = 1.f;
                 if (i == 0) {
                     m = fmaxf(tmax, -1e30f);
@@ -687,7 +731,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 uint8_t *prow = smem + PC_OFF_P + (n & 1) * PC_P + half * 8192 + (row >> 3) * 1024 + (row & 7) * 128;
                 float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < 4; ++e) {
                     uint32_t v[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
@@ -697,7 +741,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                         sum1 += p1;
                         v[x] = pack_bf16(p0, p1);
                     }
-                    *reinterpret_cast<uint4 *>(prow + ((e ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<uint4 *>(prow + (((4 * quad + e) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                 }
                 l += sum0 + sum1;
                 fence_proxy_async();
@@ -706,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     if (!(ok = warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 18))) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 4 * quad; c < 4 * quad + 4; ++c) {
                         float o[32];
                         uint32_t r[32];
                         tmem_ld32(tmem + lane_base + PC_TM_O + 32 * c, o);
@@ -722,23 +766,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             }
             if (!ok) break;
 
-            // ---- this thread's half row: columns 256 half .. + 255
+            // ---- this thread's quarter row: columns 256 half + 128 quad .. + 127
             if (w.n()) {
-                float *xl = xm + 256;
-                xl[mine] = l;
-                if (!(ok = exchanged())) break;
-                l += xl[other];
+                if (!(ok = exchange(l))) break;
+                l = of_row([](float u, float v) { return u + v; });
                 if (!(ok = warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 23))) break;
                 tc_fence_after();
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
             uint16_t *hl = a.o_hl + (size_t(live ? t : 0) * LCA_HEADS + head) * (2 * LCA_DC) + 256 * half;
             float *po = a.part_o + (size_t(w.slot < 0 ? 0 : w.slot) * PC_ROWS + 64 * cta + row) * LCA_DC + 256 * half;
-            if (w.slot >= 0 && half == 0)
+            if (w.slot >= 0 && half == 0 && quad == 0)
                 *reinterpret_cast<float2 *>(a.part_ml + (size_t(w.slot) * PC_ROWS + 64 * cta + row) * 2) =
                     make_float2(m, l);
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 4 * quad; c < 4 * quad + 4; ++c) {
                 float o[32];
                 if (w.n()) {
                     tmem_ld32(tmem + lane_base + PC_TM_O + 32 * c, o);
