@@ -254,23 +254,50 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// mbar_wait by one lane for the whole warp (32 lanes that poll a barrier take
-// the shared-memory pipe from everybody else); the same answer in every lane.
-// The loop stands apart: with it inline at every wait and the loops over slots
-// unrolled, the warps' different roles kept evicting each other's instructions
-// (half of all stall cycles; 2.0 times the run time).
-__device__ __noinline__ bool warp_wait_more(uint32_t bar, uint32_t parity, volatile int *abort, int site)
+// One lane looks at a barrier for the whole warp (32 lanes that poll take the
+// shared-memory pipe from everybody else); the same answer in every lane.  The
+// look is predicated, not branched to: a warp whose lanes parted in a wait
+// stayed parted through the tile that followed and ran it twice.
+__device__ __forceinline__ bool warp_try_wait(uint32_t bar, uint32_t parity)
 {
-    bool ok = false;
-    if (elect_one()) ok = mbar_wait(bar, parity, abort, K_CHUNK, site);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred E, Q;\n\t"
+        "elect.sync _|E, 0xffffffff;\n\t"
+        "setp.ne.b32 Q, 0, 0;\n\t"
+        "@E mbarrier.try_wait.parity.shared::cta.b64 Q, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, Q;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
     return __any_sync(0xffffffffu, ok);
 }
 
+// The loop stands apart: with it inline at every wait and the loops over slots
+// unrolled, the warps' roles kept evicting each other's instructions.  The
+// clock is read only after many looks: a read of %globaltimer takes long.
+__device__ __noinline__ bool warp_wait_more(uint32_t bar, uint32_t parity, volatile int *abort, int site)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (warp_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0) {
+            if (__any_sync(0xffffffffu, *abort != 0)) return false;
+            const uint64_t t = __shfl_sync(0xffffffffu, globaltimer(), 0);
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitLimitNs) {
+                report_timeout(K_CHUNK, site);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// mbar_wait by a whole, converged warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, int site)
 {
-    bool ok = false;
-    if (elect_one()) ok = mbar_try_wait(bar, parity);
-    ok = __any_sync(0xffffffffu, ok) || warp_wait_more(bar, parity, abort, site);
+    const bool ok = warp_try_wait(bar, parity) || warp_wait_more(bar, parity, abort, site);
     __syncwarp();
     return ok;
 }
@@ -285,6 +312,32 @@ struct RingPlace {
             slot = 0;
             par ^= 1;
         }
+    }
+    __device__ __forceinline__ void skip(uint32_t n)   // n <= N
+    {
+        slot += n;
+        if (slot >= N) {
+            slot -= N;
+            par ^= 1;
+        }
+    }
+    // How many of the next `want` places have landed (barriers from `first` on),
+    // at least one: each lane looks at a place of its own, so one look, of ~100
+    // cycles, serves several slots.  0: given up.
+    __device__ __forceinline__ int landed(uint32_t first, int want, int lane, volatile int *abort, int site) const
+    {
+        uint32_t s = slot + uint32_t(lane), q = par;
+        if (s >= N) {
+            s -= N;
+            q ^= 1;
+        }
+        const bool mine = lane < (want < N ? want : N);
+        uint32_t there = __ballot_sync(0xffffffffu, mine && mbar_test(first + 8 * s, q));
+        if (!(there & 1u)) {
+            if (!warp_wait(first + 8 * slot, par, abort, site)) return 0;
+            there = __ballot_sync(0xffffffffu, mine && mbar_test(first + 8 * s, q)) | 1u;
+        }
+        return __ffs(int(~there)) - 1;
     }
 };
 
@@ -442,26 +495,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
 
     if (warp >= PC_SOFTMAX && warp < PC_SOFTMAX + 2 * PC_PRODUCERS) {
         // ------------------------------------------------------------ producers
-        // Two warps bring S's slots in turn, two PV's: one takes about 200
-        // cycles a slot and 50 more for each further page in it, the MMAs use
-        // a slot of either ring every 250 to 280.
+        // Two warps bring S's slots in turn, two PV's (warp p a ring's uses
+        // p, p + 2, ...): the MMAs use a slot of either ring every 250 to 280
+        // cycles, about what one warp needs for wait, expect and copy.
         const uint32_t p = uint32_t(warp) & 1;
         const bool is_k = warp < PC_SOFTMAX + PC_PRODUCERS;
-        const int k_shift = min(a.page_shift, 6);
         const int64_t no_page = a.n_pages << (a.page_shift - 3);   // beyond the map: zeros
         const int64_t in_page = (int64_t(1) << a.page_shift) - 1;
+        const uint32_t ring = is_k ? PC_KRING : PC_VRING;
+        const uint32_t full0 = is_k ? kfull(0) : vfull(0), empty0 = is_k ? kempty(0) : vempty(0);
+        const uint32_t slot0 = is_k ? kaddr(0) : vaddr(0), full_pair = map_to_cta(full0, 0);
         if (lane == 0) {
             prefetch_tensormap(is_k ? &map_k : &map_v);
             if (is_k && p == 0) prefetch_tensormap(&map_q);
         }
-        const int ring = is_k ? PC_KRING : PC_VRING;
-        const uint32_t first_full = is_k ? kfull(0) : vfull(0), first_empty = is_k ? kempty(0) : vempty(0);
-        const uint32_t first_slot = is_k ? kaddr(0) : vaddr(0);
-        // copies into a slot: the pages in a K slot's 64 rows; a V slot's 16 rows lie in one
-        const int copies = is_k ? 64 >> k_shift : 1;
-        const CUtensorMap *map = is_k ? &map_k : &map_v;
-        uint32_t n = 0, x = 0, slot = 0, par = 0;   // tiles, ring uses; x's slot and its parity
+        uint32_t n = 0, x = p;           // tiles; this warp's next use of the ring
+        uint32_t slot = p, par = 1;      // its slot, and the parity that says that it is free
+        uint32_t base = 0;               // the tile's first use
         bool ok = true;
+        // the slot of use x is free
+        const auto take = [&]() {
+            ok = warp_wait(empty0 + 8 * slot, par, abort_flag, 2);
+            return ok;
+        };
+        const auto step = [&]() {
+            x += PC_PRODUCERS;
+            slot += PC_PRODUCERS;
+            if (slot >= ring) {
+                slot -= ring;
+                par ^= 1;
+            }
+        };
         while (ok && range.next(a.plan, w)) {
             if (w.n() == 0) continue;
             if (is_k && p == 0) {
@@ -478,45 +542,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             PageWindow win;
             win.open(a.block_table + size_t(w.t.b) * size_t(a.max_blocks), row0 >> a.page_shift, a.max_blocks, a.n_pages,
                      lane);
+            const auto group_of = [&](int64_t row) {
+                const int32_t page = win.at(row >> a.page_shift, lane);
+                return int(page >= 0 ? ((int64_t(page) << a.page_shift) + (row & in_page)) >> 3 : no_page);
+            };
             for (int i = 0; i < w.n() && ok; ++i, ++n, row0 += PC_TILE) {
-                const int parts = is_k ? PC_KS : w.v_slots(i, max_rows);
+                if (is_k) {
+                    // the 64 rows lie in one page, or in 2 or 4
+                    const int g0 = group_of(row0);
+                    int g1 = 0, g2 = 0, g3 = 0;
+                    if (a.page_shift < 6) g1 = group_of(row0 + (a.page_shift == 5 ? 32 : 16));
+                    if (a.page_shift < 5) {
+                        g2 = group_of(row0 + 32);
+                        g3 = group_of(row0 + 48);
+                    }
 #pragma unroll 1
-                for (int part = 0; part < parts; ++part, ++x) {
-                    if ((x & 1) == p) {
-                        if (!(ok = warp_wait(first_empty + 8 * slot, par ^ 1, abort_flag, 2))) break;
-                        const uint32_t bar = map_to_cta(first_full + 8 * slot, 0), dst = first_slot + slot * PC_SLOT;
-                        if (cta == 0 && elect_one()) mbar_expect_tx(first_full + 8 * slot, 2 * PC_SLOT);
-#pragma unroll 1
-                        for (int c = 0; c < copies; ++c) {
-                            const int64_t r = row0 + (is_k ? int64_t(c) << k_shift : 16 * part);
-                            const int32_t page = win.at(r >> a.page_shift, lane);
-                            const int64_t group =
-                                page >= 0 ? ((int64_t(page) << a.page_shift) + (r & in_page)) >> 3 : no_page;
-                            if (elect_one())
-                                tma_load_4d_pair(dst + ((c << k_shift) >> 3) * 1024, map, bar, 0, 0,
-                                                 is_k ? part : 4 * int(cta), int(group));
+                    for (; x < base + PC_KS; step()) {
+                        if (!take()) break;
+                        if (elect_one()) {
+                            const int part = int(x - base);
+                            const uint32_t dst = slot0 + slot * PC_SLOT, bar = full_pair + 8 * slot;
+                            if (cta == 0) mbar_expect_tx(full0 + 8 * slot, 2 * PC_SLOT);   // both CTAs' bytes
+                            tma_load_4d_pair(dst, &map_k, bar, 0, 0, part, g0);
+                            if (a.page_shift < 6)
+                                tma_load_4d_pair(dst + (a.page_shift == 5 ? 4096 : 2048), &map_k, bar, 0, 0, part, g1);
+                            if (a.page_shift < 5) {
+                                tma_load_4d_pair(dst + 4096, &map_k, bar, 0, 0, part, g2);
+                                tma_load_4d_pair(dst + 6144, &map_k, bar, 0, 0, part, g3);
+                            }
                         }
+                        __syncwarp();
                     }
-                    if (++slot == uint32_t(ring)) {
-                        slot = 0;
-                        par ^= 1;
+                    base += PC_KS;
+                } else {
+                    const uint32_t end = base + uint32_t(w.v_slots(i, max_rows));
+#pragma unroll 1
+                    for (; x < end; step()) {
+                        const int g = group_of(row0 + 16 * int(x - base));   // 16 rows lie in one page
+                        if (!take()) break;
+                        if (elect_one()) {
+                            if (cta == 0) mbar_expect_tx(full0 + 8 * slot, 2 * PC_SLOT);
+                            tma_load_4d_pair(slot0 + slot * PC_SLOT, &map_v, full_pair + 8 * slot, 0, 0, 4 * int(cta), g);
+                        }
+                        __syncwarp();
                     }
+                    base = end;
                 }
             }
         }
-        // no copy left in flight, and every commit that arrives at this CTA
-        // has: this warp's among the ring's last uses, backwards
+        // No copy left in flight, and every commit that arrives at this CTA
+        // has: this warp's among the ring's last uses, backwards.
 #pragma unroll 1
-        for (int back = 0; back < ring && x > 0 && ok; ++back) {
-            --x;
-            if (slot == 0) {
-                slot = uint32_t(ring);
+        while (ok && x >= PC_PRODUCERS && x - PC_PRODUCERS + ring >= base) {
+            x -= PC_PRODUCERS;
+            if (slot < PC_PRODUCERS) {
+                slot += ring;
                 par ^= 1;
             }
-            --slot;
-            if ((x & 1) != p) continue;
-            if (cta == 0) ok = warp_wait(first_full + 8 * slot, par, abort_flag, 4);
-            ok = ok && warp_wait(first_empty + 8 * slot, par, abort_flag, 6);
+            slot -= PC_PRODUCERS;
+            if (cta == 0) ok = warp_wait(full0 + 8 * slot, par ^ 1, abort_flag, 4);
+            ok = ok && warp_wait(empty0 + 8 * slot, par ^ 1, abort_flag, 6);
         }
         if (!ok) {   // given up: copies may still be under way
             const uint64_t t0 = globaltimer();
@@ -527,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
         constexpr uint32_t IDESC_S = idesc_bf16(PC_ROWS, PC_TILE, 0, 0);
         RingPlace<PC_KRING> at;
         uint32_t n = 0, pieces = 0;
-        bool ok = true, there = false;   // there: the slot has been seen to have landed
+        bool ok = true;
         while (ok && range.next(a.plan, w)) {
             const int m = __shfl_sync(0xffffffffu, w.n(), 0);
             if (m == 0) continue;
@@ -535,23 +620,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             for (int i = 0; i < m && ok; ++i, ++n) {
                 if (!(ok = warp_wait(sread(n), ((n >> 1) & 1) ^ 1, abort_flag, 9))) break;
                 const uint32_t d = tmem + PC_TM_S + 64 * (n & 1);
-#pragma unroll 1
-                for (int c = 0; c < PC_KS; ++c) {
-                    if (!there && !(ok = warp_wait(kfull(at.slot), at.par, abort_flag, 10))) break;
+                for (int c = 0; c < PC_KS;) {
+                    const int got = at.landed(kfull(0), PC_KS - c, lane, abort_flag, 10);
+                    if (!(ok = got > 0)) break;
                     tc_fence_after();
-                    const RingPlace<PC_KRING> now = at;
-                    ++at;
-                    bool next = false;
                     if (elect_one()) {
-                        next = mbar_test(kfull(at.slot), at.par);   // its ~100 cycles pass under the MMAs
-                        const uint64_t qd = sdesc_sw128(sbase + c * 8192, 16, 1024);
-                        const uint64_t kd = sdesc_sw128(kaddr(now.slot), 16, 1024);
+                        RingPlace<PC_KRING> now = at;
+#pragma unroll 1
+                        for (int x = c; x < c + got; ++x, ++now) {
+                            const uint64_t qd = sdesc_sw128(sbase + x * 8192, 16, 1024);
+                            const uint64_t kd = sdesc_sw128(kaddr(now.slot), 16, 1024);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) mma2_ss(d, qd + 2 * ks, kd + 2 * ks, IDESC_S, c + ks ? 1u : 0u);
-                        tc_commit_pair(kempty(now.slot));
-                        if (c == PC_KS - 1) tc_commit_pair(sdone(n));
+                            for (int ks = 0; ks < 4; ++ks) mma2_ss(d, qd + 2 * ks, kd + 2 * ks, IDESC_S, x + ks ? 1u : 0u);
+                            tc_commit_pair(kempty(now.slot));
+                        }
+                        if (c + got == PC_KS) tc_commit_pair(sdone(n));
                     }
-                    there = __any_sync(0xffffffffu, next);
+                    __syncwarp();
+                    c += got;
+                    at.skip(uint32_t(got));
                 }
             }
             ++pieces;
@@ -587,26 +674,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 }
                 if (i == 0 && !(ok = warp_wait(oread, (pieces & 1) ^ 1, abort_flag, 12))) break;
                 if (!(ok = warp_wait(pfull(n), (n >> 1) & 1, abort_flag, 13))) break;
-                bool there = false;
                 const uint32_t pst = sbase + PC_OFF_P + (n & 1) * PC_P;
-#pragma unroll 1
-                for (int v = 0; v < nvs; ++v) {
-                    if (!there && !(ok = warp_wait(vfull(at.slot), at.par, abort_flag, 14))) break;
+                for (int v = 0; v < nvs;) {
+                    const int got = at.landed(vfull(0), nvs - v, lane, abort_flag, 14);
+                    if (!(ok = got > 0)) break;
                     tc_fence_after();
-                    const RingPlace<PC_VRING> now = at;
-                    ++at;
-                    bool next = false;
                     if (elect_one()) {
-                        next = mbar_test(vfull(at.slot), at.par);
-                        const uint64_t pd = sdesc_sw128(pst + (v >> 2) * 8192 + (v & 3) * 32, 16, 1024);
-                        const uint64_t vd = sdesc_sw128(vaddr(now.slot), 1024, 4096);
+                        RingPlace<PC_VRING> now = at;
+#pragma unroll 1
+                        for (int x = v; x < v + got; ++x, ++now) {
+                            const uint64_t pd = sdesc_sw128(pst + (x >> 2) * 8192 + (x & 3) * 32, 16, 1024);
+                            const uint64_t vd = sdesc_sw128(vaddr(now.slot), 1024, 4096);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            mma2_ss(tmem + PC_TM_O + 128 * j, pd, vd + 128 * j, IDESC_PV, (i > 0 || v > 0) ? 1u : 0u);
-                        tc_commit_pair(vempty(now.slot));
-                        if (v == nvs - 1) tc_commit_pair(vdone(n));
+                            for (int j = 0; j < 2; ++j)
+                                mma2_ss(tmem + PC_TM_O + 128 * j, pd, vd + 128 * j, IDESC_PV, (i > 0 || x > 0) ? 1u : 0u);
+                            tc_commit_pair(vempty(now.slot));
+                        }
+                        if (v + got == nvs) tc_commit_pair(vdone(n));
                     }
-                    there = __any_sync(0xffffffffu, next);
+                    __syncwarp();
+                    v += got;
+                    at.skip(uint32_t(got));
                 }
             }
             ++pieces;
