@@ -12,9 +12,8 @@
 // Neither Q nor P nor the accumulators cross between the SMs.  The accumulator
 // of 64 x 512 fp32 takes 256 columns of tensor memory, spread over all 128
 // lanes (lanes 0-63 hold rows 0-63 and the columns of the first half of N,
-// lanes 64-127 the same rows and the second half); two softmax threads share a
-// lane's columns, so each owns a quarter of a row: 32 of the 128 logits, 128
-// of the 512 outputs.
+// lanes 64-127 the same rows and the second half), so a softmax thread owns
+// half a row: 64 of the 128 logits, 256 of the 512 outputs.
 //
 // A tile is fetched in slots of 8 KB: nine for S ([64 rows][64 columns], this
 // CTA's rows) and eight for PV ([16 rows][256 columns], this CTA's columns),
@@ -22,6 +21,8 @@
 // slots each: only where one warp uses and frees a ring's slots in order does
 // the parity of a slot's barrier tell two of its uses apart.
 #pragma once
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace lca {
@@ -39,18 +40,18 @@ constexpr int PC_SLOTS = PC_KRING + PC_VRING;
 constexpr int PC_P = 2 * 8192;                   // P [64 x 128] bf16, two [64 x 64] blocks
 constexpr int PC_OFF_P = PC_Q;
 constexpr int PC_OFF_RING = PC_OFF_P + 2 * PC_P;
-constexpr int PC_OFF_X = PC_OFF_RING + PC_SLOTS * PC_SLOT;   // [2][256] row maxima or sums
-constexpr int PC_OFF_BAR = PC_OFF_X + 2 * 256 * 4;
-constexpr int PC_BARS = 2 * PC_SLOTS + 15;
+constexpr int PC_OFF_X = PC_OFF_RING + PC_SLOTS * PC_SLOT;   // [2][128] row maxima or sums
+constexpr int PC_OFF_BAR = PC_OFF_X + 2 * 128 * 4;
+constexpr int PC_BARS = 2 * PC_SLOTS + 13;
 constexpr int PC_OFF_MISC = PC_OFF_BAR + 8 * PC_BARS;
 constexpr int PC_SMEM = PC_OFF_MISC + 16;
 constexpr int PC_SMEM_ALLOC = PC_SMEM;   // no room to align it: the kernel checks that it starts at 1024 bytes
 static_assert(PC_SMEM_ALLOC <= 227 * 1024, "one CTA per SM");
 constexpr uint32_t PC_TM_O = 0, PC_TM_S = 256;   // O 256 columns, S two buffers of 64
-constexpr int PC_SOFTMAX = 8;                    // warps 0 .. 7
-constexpr int PC_PRODUCERS = 2;                  // warps 8, 9 for S, 10, 11 for PV
-constexpr int PC_WARP_S = 12, PC_WARP_PV = 13;   // MMA issue (CTA 0)
-constexpr int PC_THREADS = 32 * 14;
+constexpr int PC_SOFTMAX = 4;                    // warps 0 .. 3
+constexpr int PC_KWARPS = 3, PC_VWARPS = 2;      // fetch: warps 4 .. 6 for S, 7, 8 for PV
+constexpr int PC_WARP_S = 9, PC_WARP_PV = 10;    // MMA issue (CTA 0)
+constexpr int PC_THREADS = 32 * 11;
 constexpr int PC_MAX_CLUSTERS = 80;              // partial outputs: two per cluster
 constexpr int PC_OVER = 2;                       // cost of a piece beyond its tiles, in tiles
 
@@ -294,6 +295,25 @@ __device__ __noinline__ bool warp_wait_more(uint32_t bar, uint32_t parity, volat
     }
 }
 
+// The same for one thread.
+__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, volatile int *abort, int site)
+{
+    uint64_t t0 = 0;
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0) {
+            if (*abort) return false;
+            const uint64_t t = globaltimer();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitLimitNs) {
+                report_timeout(K_CHUNK, site);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // mbar_wait by a whole, converged warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort, int site)
 {
@@ -321,23 +341,24 @@ struct RingPlace {
             par ^= 1;
         }
     }
-    // How many of the next `want` places have landed (barriers from `first` on),
-    // at least one: each lane looks at a place of its own, so one look, of ~100
-    // cycles, serves several slots.  0: given up.
-    __device__ __forceinline__ int landed(uint32_t first, int want, int lane, volatile int *abort, int site) const
+    // Each lane looks at a place of its own, `ahead` and more places on (barriers
+    // from `first` on): one look, of ~100 cycles, serves several slots.
+    __device__ __forceinline__ bool look(uint32_t first, int ahead, int lane) const
     {
-        uint32_t s = slot + uint32_t(lane), q = par;
+        uint32_t s = slot + uint32_t(ahead + lane), q = par;
         if (s >= N) {
             s -= N;
             q ^= 1;
         }
-        const bool mine = lane < (want < N ? want : N);
-        uint32_t there = __ballot_sync(0xffffffffu, mine && mbar_test(first + 8 * s, q));
-        if (!(there & 1u)) {
-            if (!warp_wait(first + 8 * slot, par, abort, site)) return 0;
-            there = __ballot_sync(0xffffffffu, mine && mbar_test(first + 8 * s, q)) | 1u;
-        }
-        return __ffs(int(~there)) - 1;
+        return ahead + lane < N && mbar_test(first + 8 * s, q);
+    }
+    // How many places in a row were complete in a look; if none is, waits for the
+    // next one.  0: given up.
+    __device__ __forceinline__ int count(uint32_t first, bool looked, volatile int *abort, int site) const
+    {
+        const uint32_t there = __ballot_sync(0xffffffffu, looked);
+        if (there & 1u) return __ffs(int(~there)) - 1;
+        return warp_wait(first + 8 * slot, par, abort, site) ? 1 : 0;
     }
 };
 
@@ -376,6 +397,33 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const CUtensorMap
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
+}
+
+// Pairs of fp32 values: two multiply-adds or adds in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // 32-byte store of eight 32-bit values.
@@ -465,13 +513,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     const uint32_t oread = BAR(B0 + 9);
     const uint32_t vready = BAR(B0 + 10);   // in both CTAs: an edge tile's PV slots have landed
     const uint32_t drain_s = BAR(B0 + 11), drain_pv = BAR(B0 + 12);
-    // the four softmax warps that share their rows have written what they exchange
-    const uint32_t xchg = BAR(B0 + 13 + (warp & 1));
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + PC_OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + PC_OFF_MISC + 4);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < PC_BARS; ++i) mbar_init(BAR(i), i < B0 + 5 ? 1 : i <= B0 + 9 ? 2 * PC_SOFTMAX : i <= B0 + 12 ? 1 : PC_SOFTMAX / 2);
+        for (int i = 0; i < PC_BARS; ++i) mbar_init(BAR(i), i < B0 + 5 ? 1 : i <= B0 + 9 ? 2 * PC_SOFTMAX : 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -493,123 +539,143 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     ChunkRange range(a.plan, int(blockIdx.x >> 1), int(gridDim.x >> 1));
     ChunkPiece w;
 
-    if (warp >= PC_SOFTMAX && warp < PC_SOFTMAX + 2 * PC_PRODUCERS) {
-        // ------------------------------------------------------------ producers
-        // Two warps bring S's slots in turn, two PV's (warp p a ring's uses
-        // p, p + 2, ...): the MMAs use a slot of either ring every 250 to 280
-        // cycles, about what one warp needs for wait, expect and copy.
-        const uint32_t p = uint32_t(warp) & 1;
-        const bool is_k = warp < PC_SOFTMAX + PC_PRODUCERS;
-        const int64_t no_page = a.n_pages << (a.page_shift - 3);   // beyond the map: zeros
-        const int64_t in_page = (int64_t(1) << a.page_shift) - 1;
-        const uint32_t ring = is_k ? PC_KRING : PC_VRING;
-        const uint32_t full0 = is_k ? kfull(0) : vfull(0), empty0 = is_k ? kempty(0) : vempty(0);
-        const uint32_t slot0 = is_k ? kaddr(0) : vaddr(0), full_pair = map_to_cta(full0, 0);
-        if (lane == 0) {
-            prefetch_tensormap(is_k ? &map_k : &map_v);
-            if (is_k && p == 0) prefetch_tensormap(&map_q);
-        }
-        uint32_t n = 0, x = p;           // tiles; this warp's next use of the ring
-        uint32_t slot = p, par = 1;      // its slot, and the parity that says that it is free
-        uint32_t base = 0;               // the tile's first use
+    // ---------------------------------------------------------------- producers
+    // One thread each; producer p of STEP brings a ring's uses p, p + STEP, ...
+    // (wait, expect and copy take it ~400 cycles a slot; the MMAs use a slot of
+    // either ring every 250 to 280).  STEP < ring, so a producer has seen the use
+    // before last of its next slot freed.
+    const auto produce = [&](auto is_k_, uint32_t p) {
+        constexpr bool K = decltype(is_k_)::value;
+        constexpr uint32_t RING = K ? PC_KRING : PC_VRING, STEP = K ? PC_KWARPS : PC_VWARPS;
+        static_assert(STEP < RING && PC_KS % PC_KWARPS == 0 && PC_VS % PC_VWARPS == 0, "slots per tile and producer");
+        const uint32_t full0 = K ? kfull(0) : vfull(0), empty0 = K ? kempty(0) : vempty(0);
+        const uint32_t slot0 = K ? kaddr(0) : vaddr(0), full_pair = map_to_cta(full0, 0);
+        // rows, pages and 8-row groups are below 2^31
+        const int shift = a.page_shift, in_page = (1 << shift) - 1, blocks = int(a.max_blocks), pages = int(a.n_pages);
+        const int no_page = pages << (shift - 3);   // beyond the map: zeros
+        prefetch_tensormap(K ? &map_k : &map_v);
+        if (K && p == 0) prefetch_tensormap(&map_q);
+        uint32_t n = 0, x = p, base = 0;   // tiles; this producer's next use of the ring; the tile's first use
+        uint32_t slot = p, par = 1;        // x's slot, and the parity that says that it is free
         bool ok = true;
-        // the slot of use x is free
         const auto take = [&]() {
-            ok = warp_wait(empty0 + 8 * slot, par, abort_flag, 2);
+            if (!mbar_try_wait(empty0 + 8 * slot, par)) ok = wait_more(empty0 + 8 * slot, par, abort_flag, 2);
+            if (ok && cta == 0) mbar_expect_tx(full0 + 8 * slot, 2 * PC_SLOT);   // both CTAs' bytes
             return ok;
         };
         const auto step = [&]() {
-            x += PC_PRODUCERS;
-            slot += PC_PRODUCERS;
-            if (slot >= ring) {
-                slot -= ring;
+            x += STEP;
+            slot += STEP;
+            if (slot >= RING) {
+                slot -= RING;
                 par ^= 1;
             }
         };
         while (ok && range.next(a.plan, w)) {
             if (w.n() == 0) continue;
-            if (is_k && p == 0) {
+            if (K && p == 0) {
                 // the queries' buffer is free once the last S that read it is done
-                if (n > 0) ok = warp_wait(sdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 1);
+                if (n > 0) ok = wait_more(sdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 1);
                 if (!ok) break;
-                if (elect_one()) {
-                    if (cta == 0) mbar_expect_tx(qfull, 2 * PC_Q);
-                    tma_load_4d_pair(sbase, &map_q, map_to_cta(qfull, 0), 0, LCA_HEADS * (w.t.t0 + 4 * int(cta)), 0, 0);
-                }
-                __syncwarp();
+                if (cta == 0) mbar_expect_tx(qfull, 2 * PC_Q);
+                tma_load_4d_pair(sbase, &map_q, map_to_cta(qfull, 0), 0, LCA_HEADS * (w.t.t0 + 4 * int(cta)), 0, 0);
             }
-            int64_t row0 = int64_t(w.k0) * PC_TILE + (is_k ? 64 * int(cta) : 0);
-            PageWindow win;
-            win.open(a.block_table + size_t(w.t.b) * size_t(a.max_blocks), row0 >> a.page_shift, a.max_blocks, a.n_pages,
-                     lane);
-            const auto group_of = [&](int64_t row) {
-                const int32_t page = win.at(row >> a.page_shift, lane);
-                return int(page >= 0 ? ((int64_t(page) << a.page_shift) + (row & in_page)) >> 3 : no_page);
+            const int32_t *table = a.block_table + size_t(w.t.b) * size_t(a.max_blocks);
+            // (an entry is looked at only when it is used, a tile later: no wait for the load)
+            const auto page_of = [&](int r) { return (r >> shift) < blocks ? __ldg(table + (r >> shift)) : -1; };
+            const auto group_of = [&](int page, int r) {
+                return uint32_t(page) < uint32_t(pages) ? (page << (shift - 3)) + ((r & in_page) >> 3) : no_page;
             };
-            for (int i = 0; i < w.n() && ok; ++i, ++n, row0 += PC_TILE) {
-                if (is_k) {
-                    // the 64 rows lie in one page, or in 2 or 4
-                    const int g0 = group_of(row0);
-                    int g1 = 0, g2 = 0, g3 = 0;
-                    if (a.page_shift < 6) g1 = group_of(row0 + (a.page_shift == 5 ? 32 : 16));
-                    if (a.page_shift < 5) {
-                        g2 = group_of(row0 + 32);
-                        g3 = group_of(row0 + 48);
-                    }
+            // The rows that this producer brings of a tile lie in up to four
+            // pages; those of the next tile are looked up a tile ahead.  K: all 64
+            // rows in steps of `sub`; V: the 16 rows of each of its parts.
+            const int sub = K ? min(64, 1 << shift) : 16 * int(STEP);
+            constexpr int LOOKUPS = K ? 4 : PC_VS / PC_VWARPS;
+            int row0 = w.k0 * PC_TILE + (K ? 64 * int(cta) : 16 * int(x - base));
+            int page[LOOKUPS], group[LOOKUPS];
+#pragma unroll
+            for (int c = 0; c < LOOKUPS; ++c) page[c] = !K || c * sub < 64 ? page_of(row0 + c * sub) : -1;
+            const int last = w.v_slots(w.n() - 1, max_rows);
+            for (int i = w.n(); i > 0 && ok; --i, ++n, row0 += PC_TILE) {
+#pragma unroll
+                for (int c = 0; c < LOOKUPS; ++c) group[c] = group_of(page[c], row0 + c * sub);
+#pragma unroll
+                for (int c = 0; c < LOOKUPS; ++c)
+                    if (i > 1 && (!K || c * sub < 64)) page[c] = page_of(row0 + PC_TILE + c * sub);
+                if (K) {
+                    if (sub == 64) {
+#pragma unroll
+                        for (int c = 0; c < PC_KS / PC_KWARPS; ++c, step())
+                            if (ok && take())
+                                tma_load_4d_pair(slot0 + slot * PC_SLOT, &map_k, full_pair + 8 * slot, 0, 0,
+                                                 int(p) + PC_KWARPS * c, group[0]);
+                    } else {
 #pragma unroll 1
-                    for (; x < base + PC_KS; step()) {
-                        if (!take()) break;
-                        if (elect_one()) {
-                            const int part = int(x - base);
+                        for (int c = 0; c < PC_KS / PC_KWARPS; ++c, step()) {
+                            if (!ok || !take()) continue;
+                            const int part = int(p) + PC_KWARPS * c;
                             const uint32_t dst = slot0 + slot * PC_SLOT, bar = full_pair + 8 * slot;
-                            if (cta == 0) mbar_expect_tx(full0 + 8 * slot, 2 * PC_SLOT);   // both CTAs' bytes
-                            tma_load_4d_pair(dst, &map_k, bar, 0, 0, part, g0);
-                            if (a.page_shift < 6)
-                                tma_load_4d_pair(dst + (a.page_shift == 5 ? 4096 : 2048), &map_k, bar, 0, 0, part, g1);
-                            if (a.page_shift < 5) {
-                                tma_load_4d_pair(dst + 4096, &map_k, bar, 0, 0, part, g2);
-                                tma_load_4d_pair(dst + 6144, &map_k, bar, 0, 0, part, g3);
+                            tma_load_4d_pair(dst, &map_k, bar, 0, 0, part, group[0]);
+                            tma_load_4d_pair(dst + sub * 128, &map_k, bar, 0, 0, part, group[1]);
+                            if (sub == 16) {
+                                tma_load_4d_pair(dst + 4096, &map_k, bar, 0, 0, part, group[2]);
+                                tma_load_4d_pair(dst + 6144, &map_k, bar, 0, 0, part, group[3]);
                             }
                         }
-                        __syncwarp();
                     }
                     base += PC_KS;
                 } else {
-                    const uint32_t end = base + uint32_t(w.v_slots(i, max_rows));
-#pragma unroll 1
-                    for (; x < end; step()) {
-                        const int g = group_of(row0 + 16 * int(x - base));   // 16 rows lie in one page
-                        if (!take()) break;
-                        if (elect_one()) {
-                            if (cta == 0) mbar_expect_tx(full0 + 8 * slot, 2 * PC_SLOT);
-                            tma_load_4d_pair(slot0 + slot * PC_SLOT, &map_v, full_pair + 8 * slot, 0, 0, 4 * int(cta), g);
+                    const uint32_t end = base + uint32_t(i > 1 ? PC_VS : last);
+#pragma unroll
+                    for (int c = 0; c < LOOKUPS; ++c)
+                        if (ok && x < end && take()) {
+                            tma_load_4d_pair(slot0 + slot * PC_SLOT, &map_v, full_pair + 8 * slot, 0, 0, 4 * int(cta),
+                                             group[c]);
+                            step();
                         }
-                        __syncwarp();
-                    }
                     base = end;
                 }
             }
         }
         // No copy left in flight, and every commit that arrives at this CTA
-        // has: this warp's among the ring's last uses, backwards.
-#pragma unroll 1
-        while (ok && x >= PC_PRODUCERS && x - PC_PRODUCERS + ring >= base) {
-            x -= PC_PRODUCERS;
-            if (slot < PC_PRODUCERS) {
-                slot += ring;
+        // has: this producer's among the ring's last uses, backwards.
+        while (ok && x >= STEP && x - STEP + RING >= base) {
+            x -= STEP;
+            if (slot < STEP) {
+                slot += RING;
                 par ^= 1;
             }
-            slot -= PC_PRODUCERS;
-            if (cta == 0) ok = warp_wait(full0 + 8 * slot, par ^ 1, abort_flag, 4);
-            ok = ok && warp_wait(empty0 + 8 * slot, par ^ 1, abort_flag, 6);
+            slot -= STEP;
+            if (cta == 0) ok = wait_more(full0 + 8 * slot, par ^ 1, abort_flag, 4);
+            ok = ok && wait_more(empty0 + 8 * slot, par ^ 1, abort_flag, 6);
         }
         if (!ok) {   // given up: copies may still be under way
             const uint64_t t0 = globaltimer();
             while (globaltimer() - t0 < 10000000ull) __nanosleep(1000);
         }
+    };
+
+    if (warp >= PC_SOFTMAX && warp < PC_SOFTMAX + PC_KWARPS) {
+        if (lane == 0) produce(std::true_type{}, uint32_t(warp - PC_SOFTMAX));
+        __syncwarp();
+    } else if (warp >= PC_SOFTMAX + PC_KWARPS && warp < PC_WARP_S) {
+        if (lane == 0) produce(std::false_type{}, uint32_t(warp - PC_SOFTMAX - PC_KWARPS));
+        __syncwarp();
     } else if (warp == PC_WARP_S && cta == 0) {
         // ------------------------------------------------------------ S = Q . tile^T for the pair
         constexpr uint32_t IDESC_S = idesc_bf16(PC_ROWS, PC_TILE, 0, 0);
+        const uint64_t q_desc = sdesc_sw128(sbase, 16, 1024), k_desc = sdesc_sw128(kaddr(0), 16, 1024);
+        // chunks c .. c + count - 1 of a tile, from slot `at` on
+        const auto s_mmas = [&](RingPlace<PC_KRING> at, uint32_t d, int c, int count) {
+            uint64_t qd = q_desc + uint64_t(c * (8192 >> 4));
+#pragma unroll 1
+            for (; count > 0; --count, ++c, ++at, qd += 8192 >> 4) {
+                const uint64_t kd = k_desc + uint64_t(at.slot * (PC_SLOT >> 4));
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) mma2_ss(d, qd + 2 * ks, kd + 2 * ks, IDESC_S, c + ks ? 1u : 0u);
+                tc_commit_pair(kempty(at.slot));
+            }
+        };
         RingPlace<PC_KRING> at;
         uint32_t n = 0, pieces = 0;
         bool ok = true;
@@ -620,25 +686,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             for (int i = 0; i < m && ok; ++i, ++n) {
                 if (!(ok = warp_wait(sread(n), ((n >> 1) & 1) ^ 1, abort_flag, 9))) break;
                 const uint32_t d = tmem + PC_TM_S + 64 * (n & 1);
+                bool looked = at.look(kfull(0), 0, lane);
                 for (int c = 0; c < PC_KS;) {
-                    const int got = at.landed(kfull(0), PC_KS - c, lane, abort_flag, 10);
+                    const int got = min(at.count(kfull(0), looked, abort_flag, 10), PC_KS - c);
                     if (!(ok = got > 0)) break;
                     tc_fence_after();
+                    if (got > 1 && elect_one()) s_mmas(at, d, c, got - 1);
+                    __syncwarp();
+                    c += got - 1;
+                    at.skip(uint32_t(got - 1));
+                    looked = at.look(kfull(0), 1, lane);   // comes back while the last one's MMAs are issued
                     if (elect_one()) {
-                        RingPlace<PC_KRING> now = at;
-#pragma unroll 1
-                        for (int x = c; x < c + got; ++x, ++now) {
-                            const uint64_t qd = sdesc_sw128(sbase + x * 8192, 16, 1024);
-                            const uint64_t kd = sdesc_sw128(kaddr(now.slot), 16, 1024);
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) mma2_ss(d, qd + 2 * ks, kd + 2 * ks, IDESC_S, x + ks ? 1u : 0u);
-                            tc_commit_pair(kempty(now.slot));
-                        }
-                        if (c + got == PC_KS) tc_commit_pair(sdone(n));
+                        s_mmas(at, d, c, 1);
+                        if (c + 1 == PC_KS) tc_commit_pair(sdone(n));
                     }
                     __syncwarp();
-                    c += got;
-                    at.skip(uint32_t(got));
+                    ++c;
+                    at.skip(1);
                 }
             }
             ++pieces;
@@ -654,6 +718,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     } else if (warp == PC_WARP_PV && cta == 0) {
         // ------------------------------------------------------------ O += P . tile for the pair
         constexpr uint32_t IDESC_PV = idesc_bf16(PC_ROWS, 256, 0, 1);
+        const uint64_t p_desc = sdesc_sw128(sbase + PC_OFF_P, 16, 1024), v_desc = sdesc_sw128(vaddr(0), 1024, 4096);
+        // 16-row parts v .. v + count - 1 of a tile, from slot `at` on
+        const auto pv_mmas = [&](RingPlace<PC_VRING> at, uint64_t pd, int v, int count, bool add) {
+#pragma unroll 1
+            for (; count > 0; --count, ++v, ++at) {
+                const uint64_t p = pd + uint64_t((v >> 2) * (8192 >> 4) + (v & 3) * 2);
+                const uint64_t vd = v_desc + uint64_t(at.slot * (PC_SLOT >> 4));
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    mma2_ss(tmem + PC_TM_O + 128 * j, p, vd + 128 * j, IDESC_PV, add || v > 0 ? 1u : 0u);
+                tc_commit_pair(vempty(at.slot));
+            }
+        };
         RingPlace<PC_VRING> at;
         uint32_t n = 0, pieces = 0;
         bool ok = true;
@@ -674,27 +751,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 }
                 if (i == 0 && !(ok = warp_wait(oread, (pieces & 1) ^ 1, abort_flag, 12))) break;
                 if (!(ok = warp_wait(pfull(n), (n >> 1) & 1, abort_flag, 13))) break;
-                const uint32_t pst = sbase + PC_OFF_P + (n & 1) * PC_P;
+                const uint64_t pd = p_desc + (n & 1) * (PC_P >> 4);
+                bool looked = at.look(vfull(0), 0, lane);
                 for (int v = 0; v < nvs;) {
-                    const int got = at.landed(vfull(0), nvs - v, lane, abort_flag, 14);
+                    const int got = min(at.count(vfull(0), looked, abort_flag, 14), nvs - v);
                     if (!(ok = got > 0)) break;
                     tc_fence_after();
+                    if (got > 1 && elect_one()) pv_mmas(at, pd, v, got - 1, i > 0);
+                    __syncwarp();
+                    v += got - 1;
+                    at.skip(uint32_t(got - 1));
+                    looked = at.look(vfull(0), 1, lane);
                     if (elect_one()) {
-                        RingPlace<PC_VRING> now = at;
-#pragma unroll 1
-                        for (int x = v; x < v + got; ++x, ++now) {
-                            const uint64_t pd = sdesc_sw128(pst + (x >> 2) * 8192 + (x & 3) * 32, 16, 1024);
-                            const uint64_t vd = sdesc_sw128(vaddr(now.slot), 1024, 4096);
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                mma2_ss(tmem + PC_TM_O + 128 * j, pd, vd + 128 * j, IDESC_PV, (i > 0 || x > 0) ? 1u : 0u);
-                            tc_commit_pair(vempty(now.slot));
-                        }
-                        if (v + got == nvs) tc_commit_pair(vdone(n));
+                        pv_mmas(at, pd, v, 1, i > 0);
+                        if (v + 1 == nvs) tc_commit_pair(vdone(n));
                     }
                     __syncwarp();
-                    v += got;
-                    at.skip(uint32_t(got));
+                    ++v;
+                    at.skip(1);
                 }
             }
             ++pieces;
@@ -708,58 +782,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
         __syncwarp();
     } else if (warp < PC_SOFTMAX) {
         // ------------------------------------------------------------ softmax and epilogue
-        // half: which 64 of the tile's rows and 256 of o's columns this lane of
-        // tensor memory holds; quad: which half of those is this warp's
-        const int lane4 = 32 * (warp & 3) + lane, row = lane4 & 63, half = lane4 >> 6, quad = warp >> 2;
-        const uint32_t lane_base = uint32_t(32 * (warp & 3)) << 16;
-        float *xm = reinterpret_cast<float *>(smem + PC_OFF_X);   // [2][quad][half][row]
-        const int mine = 128 * quad + lane4;
+        // (half: which 64 of the tile's rows and 256 of o's columns.)  Once a
+        // wait has given up (!ok) the loops run on without waiting or arriving
+        // anywhere but at the pair's named barrier.
+        const int lane4 = 32 * warp + lane, row = lane4 & 63, half = lane4 >> 6;
+        const uint32_t lane_base = uint32_t(32 * warp) << 16;
+        const int pair_bar = 1 + (warp & 1);   // warps w and w + 2 share their rows
+        float *xm = reinterpret_cast<float *>(smem + PC_OFF_X);
         const int tok = 4 * int(cta) + (row >> 4), head = row & 15;
         const uint32_t peer_sread = map_to_cta(sread(0), 0), peer_pfull = map_to_cta(pfull(0), 0);
         const uint32_t peer_oread = map_to_cta(oread, 0);
         const int sub_shift = min(a.page_shift, 7), subs = PC_TILE >> sub_shift;
+        const uint32_t all_pages = (1u << subs) - 1u;
         uint32_t n = 0, x0 = 0, edges = 0, swaps = 0;   // x0: first use of PV's ring
         bool ok = true;
-        // Puts this thread's value beside those of the other three that share
-        // its row (warps w + 2, w + 4, w + 6 modulo 8).  Two buffers in turn: who
-        // writes one has seen everybody past the exchange that used it last.
+        // The value of the other thread of this row.  Two buffers in turn: who
+        // writes one has seen the other past the exchange that used it last.
         const auto exchange = [&](float v) {
-            xm[(swaps & 1) * 256 + mine] = v;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(xchg);
-            return warp_wait(xchg, swaps++ & 1, abort_flag, 19);
+            float *x = xm + (swaps++ & 1) * 128;
+            x[lane4] = v;
+            named_bar_sync(pair_bar, 64);
+            return x[lane4 ^ 64];
         };
-        const auto of_row = [&](auto f) {
-            const float *v = xm + ((swaps & 1) ^ 1) * 256 + row;
-            return f(f(v[0], v[64]), f(v[128], v[192]));
-        };
-        while (ok && range.next(a.plan, w)) {
+        while (range.next(a.plan, w)) {
+            const int tiles = w.n();
             const int32_t t = w.t.t0 + tok;
             const bool live = tok < w.t.live;
             const int32_t nv = live ? clamp_rows(w.t.row_base + t, max_rows) : 0;
             // rows that every live token of the tile (of both CTAs) attends
             const int32_t nv_all = clamp_rows(w.t.row_base + w.t.t0, max_rows);
+            const int nvs_last = tiles ? w.v_slots(tiles - 1, max_rows) : 0;
             float m = -1e30f, l = 0.f;
-            PageWindow win;
-            if (w.n())
-                win.open(a.block_table + size_t(w.t.b) * size_t(a.max_blocks),
-                         (int64_t(w.k0) * PC_TILE) >> a.page_shift, a.max_blocks, a.n_pages, lane);
-            for (int i = 0; i < w.n(); ++i, ++n) {
-                const int nvs = w.v_slots(i, max_rows);
-                const int64_t row0 = int64_t(w.k0 + i) * PC_TILE;
-                // which of the tile's pages are there
-                uint32_t pages = 0;
-#pragma unroll 1
-                for (int c = 0; c < subs; ++c)
-                    if (win.at((row0 + (int64_t(c) << sub_shift)) >> a.page_shift, lane) >= 0) pages |= 1u << c;
-                const bool whole = pages == (1u << subs) - 1u;
-                if (!(ok = warp_wait(sdone(n), (n >> 1) & 1, abort_flag, 15))) break;
+            int32_t row0 = w.k0 * PC_TILE;
+            // lane c looks up the c-th of a tile's pages, a tile ahead
+            const int32_t *table = a.block_table + size_t(w.t.b) * size_t(a.max_blocks);
+            const auto page_of = [&](int32_t r) {
+                const int32_t k = (r >> a.page_shift) + (a.page_shift < 7 ? lane : 0);
+                return lane < subs && k < int32_t(a.max_blocks) ? __ldg(table + k) : -1;
+            };
+            int32_t page = tiles ? page_of(row0) : -1;
+            for (int i = 0; i < tiles; ++i, ++n, row0 += PC_TILE) {
+                const uint32_t pages = __ballot_sync(0xffffffffu, uint32_t(page) < uint32_t(a.n_pages));
+                if (i + 1 < tiles) page = page_of(row0 + PC_TILE);
+                ok = ok && warp_wait(sdone(n), (n >> 1) & 1, abort_flag, 15);
                 tc_fence_after();
-                float s[32];
-                tmem_ld32(tmem + lane_base + PC_TM_S + 64 * (n & 1) + 32 * quad, s);
+                float s[64];
+                tmem_ld64(tmem + lane_base + PC_TM_S + 64 * (n & 1), s);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(peer_sread + 8 * (n & 1));
+                if (lane == 0 && ok) mbar_arrive_pair(peer_sread + 8 * (n & 1));
 
                 const bool edge = row0 + PC_TILE > nv_all;   // the same for both CTAs
                 if (edge) {
@@ -770,42 +841,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     // clear what is not finite in this CTA's columns of them
                     // (a token that does attend the row has the NaN in its
                     // weight already).
-                    uint32_t odd = 0;
+                    const int nvs = i + 1 == tiles ? nvs_last : PC_VS;
+                    ok = ok && warp_wait(vready, edges & 1, abort_flag, 16);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (!(fabsf(s[x]) <= 3.4e38f)) odd |= 1u << x;
-                    odd = __reduce_or_sync(0xffffffffu, odd);
-                    if (!(ok = warp_wait(vready, edges & 1, abort_flag, 16))) break;
-                    while (odd) {
-                        const int r = 64 * half + 32 * quad + __ffs(int(odd)) - 1;
-                        odd &= odd - 1;
-                        if ((r >> 4) >= nvs) break;
-                        uint4 *p = reinterpret_cast<uint4 *>(smem + (vaddr((x0 + (r >> 4)) % PC_VRING) - sbase) + ((r >> 3) & 1) * 4096 +
-                                                             (lane >> 3) * 1024 + (r & 7) * 128 + (lane & 7) * 16);
-                        const uint4 v = *p;
-                        bool bad = false;
-                        for (uint32_t e : {v.x, v.y, v.z, v.w})
-                            bad |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
-                        if (__any_sync(0xffffffffu, bad)) *p = make_uint4(0u, 0u, 0u, 0u);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t odd = 0;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (!(fabsf(s[32 * h + x]) <= 3.4e38f)) odd |= 1u << x;
+                        odd = __reduce_or_sync(0xffffffffu, odd);
+                        while (odd && ok) {
+                            const int r = 64 * half + 32 * h + __ffs(int(odd)) - 1;
+                            odd &= odd - 1;
+                            if ((r >> 4) >= nvs) break;
+                            uint4 *p = reinterpret_cast<uint4 *>(smem + (vaddr((x0 + (r >> 4)) % PC_VRING) - sbase) +
+                                                                 ((r >> 3) & 1) * 4096 + (lane >> 3) * 1024 +
+                                                                 (r & 7) * 128 + (lane & 7) * 16);
+                            const uint4 v = *p;
+                            bool bad = false;
+                            for (uint32_t e : {v.x, v.y, v.z, v.w})
+                                bad |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
+                            if (__any_sync(0xffffffffu, bad)) *p = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     ++edges;
                 }
-                if (edge || !live || !whole) {
-                    const int64_t left = int64_t(nv) - row0 - 64 * half - 32 * quad;
-                    uint32_t in = left <= 0 ? 0u : left >= 32 ? ~0u : (1u << int(left)) - 1u;
+                if (edge || !live || pages != all_pages) {
+                    const int32_t left = nv - row0 - 64 * half;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)   // 16 rows lie in one page
-                        if (!((pages >> ((64 * half + 32 * quad + 16 * c) >> sub_shift)) & 1u)) in &= ~(0xffffu << (16 * c));
+                    for (int h = 0; h < 2; ++h) {
+                        const int32_t k = left - 32 * h;
+                        uint32_t in = k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u;
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (!((in >> x) & 1u)) s[x] = -INFINITY;
+                        for (int c = 0; c < 2; ++c)   // 16 rows lie in one page
+                            if (!((pages >> ((64 * half + 32 * h + 16 * c) >> sub_shift)) & 1u)) in &= ~(0xffffu << (16 * c));
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (!((in >> x) & 1u)) s[32 * h + x] = -INFINITY;
+                    }
                 }
                 float tm[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int x = 4; x < 32; ++x) tm[x & 3] = fmaxf(tm[x & 3], s[x]);
+                for (int x = 4; x < 64; x += 8)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        tm[y] = x + 4 + y < 64 ? fmaxf(fmaxf(tm[y], s[x + y]), s[x + 4 + y]) : fmaxf(tm[y], s[x + y]);
                 float tmax = fmaxf(fmaxf(tm[0], tm[1]), fmaxf(tm[2], tm[3]));
-                if (!(ok = exchange(tmax))) break;
-                tmax = of_row([](float u, float v) { return fmaxf(u, v); }) * a.sl2;
+                tmax = fmaxf(tmax, exchange(tmax)) * a.sl2;
                 float f = 1.f;
                 if (i == 0) {
                     m = fmaxf(tmax, -1e30f);
@@ -815,30 +897,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     l *= f;
                 }
                 // P(n - 2) has been used
-                if (!(ok = warp_wait(vdone(n), ((n >> 1) & 1) ^ 1, abort_flag, 17))) break;
+                ok = ok && warp_wait(vdone(n), ((n >> 1) & 1) ^ 1, abort_flag, 17);
                 uint8_t *prow = smem + PC_OFF_P + (n & 1) * PC_P + half * 8192 + (row >> 3) * 1024 + (row & 7) * 128;
-                float sum0 = 0.f, sum1 = 0.f;
+                const uint64_t scale = pack2(a.sl2, a.sl2), shift = pack2(-m, -m);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     uint32_t v[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const float p0 = fast_exp2(fmaf(s[8 * e + 2 * x], a.sl2, -m));
-                        const float p1 = fast_exp2(fmaf(s[8 * e + 2 * x + 1], a.sl2, -m));
-                        sum0 += p0;
-                        sum1 += p1;
+                        float p0, p1;
+                        unpack2(fma2(pack2(s[8 * e + 2 * x], s[8 * e + 2 * x + 1]), scale, shift), p0, p1);
+                        p0 = fast_exp2(p0);
+                        p1 = fast_exp2(p1);
+                        sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
                         v[x] = pack_bf16(p0, p1);
                     }
-                    *reinterpret_cast<uint4 *>(prow + (((4 * quad + e) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<uint4 *>(prow + ((e ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                 }
+                float sum0, sum1;
+                unpack2(add2(sum[0], sum[1]), sum0, sum1);
                 l += sum0 + sum1;
                 fence_proxy_async();
                 if (__any_sync(0xffffffffu, f != 1.f)) {
                     // O must hold PV(n - 1) before it is rescaled
-                    if (!(ok = warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 18))) break;
+                    ok = ok && warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 18);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 4 * quad; c < 4 * quad + 4; ++c) {
+                    for (int c = 0; c < 8; ++c) {
                         float o[32];
                         uint32_t r[32];
                         tmem_ld32(tmem + lane_base + PC_TM_O + 32 * c, o);
@@ -849,28 +935,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(peer_pfull + 8 * (n & 1));
-                x0 += uint32_t(nvs);
+                if (lane == 0 && ok) mbar_arrive_pair(peer_pfull + 8 * (n & 1));
+                x0 += uint32_t(PC_VS);
             }
-            if (!ok) break;
+            x0 += uint32_t(nvs_last - (tiles ? PC_VS : 0));
 
-            // ---- this thread's quarter row: columns 256 half + 128 quad .. + 127
-            if (w.n()) {
-                if (!(ok = exchange(l))) break;
-                l = of_row([](float u, float v) { return u + v; });
-                if (!(ok = warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 23))) break;
+            // ---- this thread's half row: columns 256 half .. + 255
+            if (tiles) {
+                l += exchange(l);
+                ok = ok && warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 23);
                 tc_fence_after();
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
             uint16_t *hl = a.o_hl + (size_t(live ? t : 0) * LCA_HEADS + head) * (2 * LCA_DC) + 256 * half;
             float *po = a.part_o + (size_t(w.slot < 0 ? 0 : w.slot) * PC_ROWS + 64 * cta + row) * LCA_DC + 256 * half;
-            if (w.slot >= 0 && half == 0 && quad == 0)
+            if (w.slot >= 0 && half == 0)
                 *reinterpret_cast<float2 *>(a.part_ml + (size_t(w.slot) * PC_ROWS + 64 * cta + row) * 2) =
                     make_float2(m, l);
 #pragma unroll 1
-            for (int c = 4 * quad; c < 4 * quad + 4; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 float o[32];
-                if (w.n()) {
+                if (tiles) {
                     tmem_ld32(tmem + lane_base + PC_TM_O + 32 * c, o);
                 } else {
 #pragma unroll
@@ -900,10 +985,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     }
                 }
             }
-            if (w.n()) {
+            if (tiles) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(peer_oread);
+                if (lane == 0 && ok) mbar_arrive_pair(peer_oread);
             }
         }
     }
