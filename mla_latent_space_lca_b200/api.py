@@ -41,6 +41,9 @@ def _need(t, name, dtype, shape=None, host=False):
     """A contiguous tensor of this dtype (and shape) on the GPU, or, with
     host=True, in pinned host memory (read or written in place by the
     kernels over the host link)."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return   # the usual case at once: what follows names what is wrong
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda and not (host and t.is_pinned()):
@@ -350,10 +353,32 @@ def lca_append_token(cache, pos, rows, q=None, ring=None, slot=0, q_out=None, st
     check(rc, "lca_append_token")
 
 
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _same_device(first, names, *others):
+    """All on first's device; its index."""
+    dev = first.get_device()
+    for t in others:
+        if t.get_device() != dev:
+            bad = next(n for n, o in zip(names.split(), others) if o is t)
+            raise ValueError(f"{bad} is on {t.device}, expected {first.device}")
+    return dev
+
+
+def _kept(t, stream):
+    """t, allocated here for use on `stream`: its memory is not handed out
+    again while that stream still uses it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _on(dev, stream, fn, *args):
+    """fn(*args, stream) with dev as the current device, on `stream` or dev's
+    current stream.  (A server makes a handful of these calls per token: the
+    device guard is entered only where another device is current.)"""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _on(dev, stream, fn, *args)
+    return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
 
 
 def _pages(t):
@@ -389,7 +414,8 @@ def lca_page_tables(ctx_lens, new_lens, free_pages, taken, block_table, page_siz
         raise ValueError(f"free_pages must be [n_free] and block_table [{B}, max_blocks]")
 
     def made(t, name, dtype, size):
-        t = torch.empty(size, dtype=dtype, device=dev) if t is None else t
+        if t is None:
+            return _kept(torch.empty(size, dtype=dtype, device=dev), stream)
         _need(t, name, dtype, (size,))
         return t
 
@@ -399,15 +425,15 @@ def lca_page_tables(ctx_lens, new_lens, free_pages, taken, block_table, page_siz
     positions = made(positions, "positions", torch.int32, n)
     taken_out = made(taken_out, "taken_out", torch.int32, 1)
     counts = made(counts, "counts", torch.int32, 4)
-    _same_device(ctx_lens, new_lens=new_lens, free_pages=free_pages, taken=taken, block_table=block_table,
-                 seq_lens=seq_lens, q_start=q_start, slot_map=slot_map, positions=positions, taken_out=taken_out,
-                 counts=counts)
-    with torch.cuda.device(dev):
-        rc = _lib.lib().lca_page_tables(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages), free_pages.numel(),
-                                        _ptr(taken), _ptr(block_table), B, block_table.shape[1], int(page_size), n,
-                                        _ptr(seq_lens), _ptr(q_start), _ptr(slot_map), _ptr(positions),
-                                        _ptr(taken_out), _ptr(counts), _stream(stream))
-    check(rc, "lca_page_tables")
+    index = _same_device(ctx_lens, "new_lens free_pages taken block_table seq_lens q_start slot_map positions "
+                         "taken_out counts", new_lens, free_pages, taken, block_table, seq_lens, q_start, slot_map,
+                         positions, taken_out, counts)
+    rc = _on(index, stream, _lib.lib().lca_page_tables, ctx_lens.data_ptr(), new_lens.data_ptr(),
+             free_pages.data_ptr(), free_pages.shape[0], taken.data_ptr(), block_table.data_ptr(), B,
+             block_table.shape[1], int(page_size), n, seq_lens.data_ptr(), q_start.data_ptr(), slot_map.data_ptr(),
+             positions.data_ptr(), taken_out.data_ptr(), counts.data_ptr())
+    if rc:
+        check(rc, "lca_page_tables")
     return seq_lens, q_start, slot_map, positions, taken_out, counts
 
 
@@ -422,15 +448,16 @@ def lca_append_paged(pages, rows, slot_map, stream=None):
     if rows.dim() != 2 or rows.shape[1] != D:
         raise ValueError(f"rows has shape {tuple(rows.shape)}, expected (T, {D})")
     T = rows.shape[0]
-    pitch = rows.stride(0) if T > 1 else D
-    if rows.stride(1) != 1 or pitch < D:
+    pitch, step = rows.stride()
+    if T <= 1:
+        pitch = D
+    if step != 1 or pitch < D:
         raise ValueError(f"rows must not overlap and hold contiguous vectors (strides {rows.stride()})")
     _need(slot_map, "slot_map", torch.int64, (T,))
-    _same_device(pages, rows=rows, slot_map=slot_map)
-    with torch.cuda.device(pages.device):
-        rc = _lib.lib().lca_append_paged(_ptr(rows), pitch, _ptr(slot_map), T, _ptr(pages), pages.shape[0],
-                                         pages.shape[1], _stream(stream))
-    check(rc, "lca_append_paged")
+    rc = _on(_same_device(pages, "rows slot_map", rows, slot_map), stream, _lib.lib().lca_append_paged,
+             rows.data_ptr(), pitch, slot_map.data_ptr(), T, pages.data_ptr(), *pages.shape[:2])
+    if rc:
+        check(rc, "lca_append_paged")
 
 
 def paged_workspace(B: int, T: int, max_new: int, device=None) -> torch.Tensor:
@@ -459,16 +486,20 @@ def mla_paged_attn(pages, block_table, seq_lens, q_start, q, w_uv, max_new, scal
         raise ValueError(f"q has shape {tuple(q.shape)}, expected (T, {H}, {D})")
     T = q.shape[0]
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
-    out = torch.empty(T, H, D_V, dtype=torch.bfloat16, device=q.device) if out is None else out
-    _need(out, "out", torch.bfloat16, (T, H, D_V))
-    ws = paged_workspace(B, T, max_new, device=q.device) if ws is None else ws
-    _same_device(pages, block_table=block_table, seq_lens=seq_lens, q_start=q_start, q=q, w_uv=w_uv, out=out, ws=ws)
-    with torch.cuda.device(pages.device):
-        rc = _lib.lib().mla_paged_attn(_ptr(pages), pages.shape[0], pages.shape[1], _ptr(block_table),
-                                       block_table.shape[1], _ptr(seq_lens), _ptr(q_start), _ptr(q), _ptr(w_uv), B, T,
-                                       int(max_new), float(default_scale() if scale is None else scale), _ptr(out),
-                                       _ptr(ws), ws.numel(), _stream(stream))
-    check(rc, "mla_paged_attn")
+    if out is None:
+        out = _kept(torch.empty(T, H, D_V, dtype=torch.bfloat16, device=q.device), stream)
+    else:
+        _need(out, "out", torch.bfloat16, (T, H, D_V))
+    if ws is None:
+        ws = _kept(paged_workspace(B, T, max_new, device=q.device), stream)
+    dev = _same_device(pages, "block_table seq_lens q_start q w_uv out ws", block_table, seq_lens, q_start, q, w_uv,
+                       out, ws)
+    rc = _on(dev, stream, _lib.lib().mla_paged_attn, pages.data_ptr(), *pages.shape[:2], block_table.data_ptr(),
+             block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(), q.data_ptr(), w_uv.data_ptr(), B, T,
+             int(max_new), float(default_scale() if scale is None else scale), out.data_ptr(), ws.data_ptr(),
+             ws.numel() * ws.element_size())
+    if rc:
+        check(rc, "mla_paged_attn")
     return out
 
 
