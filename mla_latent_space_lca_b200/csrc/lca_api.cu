@@ -25,6 +25,7 @@
 #include "append.cuh"
 #include "paged.cuh"
 #include "paged_chunk.cuh"
+#include "paged_wuv.cuh"
 
 using namespace lca;
 
@@ -72,12 +73,12 @@ int current_device(DeviceInfo **out)
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_REPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_MLA, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(tail_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TD_SMEM_ALLOC) == cudaSuccess;
-        good &= cudaFuncSetAttribute(wuv_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(paged_wuv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PW_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PC_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(tables_smem(TB_MAX_BATCH))) == cudaSuccess;
         good &= cudaFuncSetAttribute(condense_kernel<CdShape::kWarps, CdShape::kSlots>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, CdShape::kSmem) == cudaSuccess;
-        good &= cudaFuncSetAttribute(wuv_gemm_kernel<>, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(wuv_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(tail_decode_kernel<>, cudaFuncAttributeMaxDynamicSharedMemorySize, TD_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(condense_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CP_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AP_SMEM_ALLOC) == cudaSuccess;
@@ -529,6 +530,7 @@ ChunkWs chunk_ws_layout(void *ws, int B, int64_t T)
     w.plan.tile = reinterpret_cast<ChunkTile *>(take((size_t(T) / PC_TOKENS + size_t(B) + 1) * sizeof(ChunkTile)));
     w.plan.first = reinterpret_cast<int32_t *>(take(PC_MAX_CLUSTERS * 4));
     w.plan.nq = reinterpret_cast<int32_t *>(take(4));
+    w.plan.merge = reinterpret_cast<ChunkMerge *>(take(PC_MAX_CLUSTERS * sizeof(ChunkMerge)));
     w.part_o = reinterpret_cast<float *>(take(size_t(2 * PC_MAX_CLUSTERS) * PC_ROWS * LCA_DC * 4));
     w.part_ml = reinterpret_cast<float *>(take(size_t(2 * PC_MAX_CLUSTERS) * PC_ROWS * 2 * 4));
     w.o_hl = reinterpret_cast<uint16_t *>(take(size_t(T) * LCA_HEADS * 2 * LCA_DC * 2));
@@ -617,11 +619,12 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
     a.part_o = w.part_o;
     a.part_ml = w.part_ml;
     const int clusters = std::min(std::max(1, dev->sms / 2), PC_MAX_CLUSTERS);
-    CUtensorMap map_q, map_k, map_v, map_a, map_w;
+    CUtensorMap map_q, map_k, map_v, map_rows, map_a, map_w;
     const uint64_t rows = uint64_t(c.n_pages) << c.shift, q_rows = uint64_t(c.T) * LCA_HEADS;
     if ((rc = make_map_rows(&map_q, c.q, q_rows, 1, q_rows, 64)) ||
         (rc = make_map_pages(&map_k, c.pages, rows, std::min(1 << c.shift, 64), 1)) ||
         (rc = make_map_pages(&map_v, c.pages, rows, 16, 4)) ||
+        (rc = make_map_pages(&map_rows, c.pages, rows, std::min(1 << c.shift, 64), LCA_D / 64)) ||
         (rc = make_map3(&map_a, w.o_hl, 2 * LCA_DC, LCA_HEADS, uint64_t(c.T), uint64_t(LCA_DC) * 4,
                         uint64_t(LCA_HEADS) * LCA_DC * 4, 64, 1, 128)) ||
         (rc = make_map3(&map_w, c.w_uv, LCA_DV, LCA_DC, LCA_HEADS, LCA_DV * 2, LCA_DC * LCA_DV * 2, 64, 64, 1)))
@@ -634,19 +637,19 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
     {
         Launch l(c.st, K_CHUNK);
         const cudaError_t e = launch_ex(paged_chunk_kernel, dim3(2 * clusters), dim3(PC_THREADS), PC_SMEM_ALLOC, c.st,
-                                        true, map_q, map_k, map_v, a);
+                                        true, map_q, map_k, map_v, map_rows, a);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     if (clusters > 1) {
         Launch l(c.st, K_MERGE);
-        const cudaError_t e = launch_ex(paged_merge_kernel, dim3(PC_ROWS * 32 / MG_THREADS, clusters - 1),
+        const cudaError_t e = launch_ex(paged_merge_kernel, dim3(PC_ROWS * 32 / MG_THREADS / MG_ROWS, clusters - 1),
                                         dim3(MG_THREADS), 0, c.st, true, a, clusters);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     Launch l(c.st, K_GEMM);
-    const cudaError_t e = launch_ex(wuv_gemm_kernel<true>, dim3(unsigned((c.T + 127) / 128), LCA_HEADS), dim3(128),
-                                    GM_SMEM_ALLOC, c.st, true, map_a, map_w, (float *)nullptr, c.T,
-                                    static_cast<uint16_t *>(c.out), c.q_start, c.B);
+    const cudaError_t e = launch_ex(paged_wuv_kernel, dim3(unsigned((c.T + 127) / 128), LCA_HEADS), dim3(128),
+                                    PW_SMEM_ALLOC, c.st, true, map_a, map_w, static_cast<uint16_t *>(c.out), c.T,
+                                    c.q_start, c.B);
     if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     return LCA_OK;
 }
@@ -1096,10 +1099,9 @@ int lca_prefill_block(const void *cache, const void *q, const void *w_uv, int B,
                                     uint64_t(LCA_HEADS) * LCA_DC * 2, 64, 1, 128)))
                     return rc;
                 Launch l(st, K_GEMM);
-                const cudaError_t e = launch_ex(wuv_gemm_kernel<>, dim3(unsigned((R + 127) / 128), LCA_HEADS),
+                const cudaError_t e = launch_ex(wuv_gemm_kernel, dim3(unsigned((R + 127) / 128), LCA_HEADS),
                                                 dim3(128), GM_SMEM_ALLOC, st, false, map_a, map_w,
-                                                out + row_out * LCA_HEADS * LCA_DV, R, (uint16_t *)nullptr,
-                                                (const int32_t *)nullptr, 0);
+                                                out + row_out * LCA_HEADS * LCA_DV, R);
                 if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
             }
         }

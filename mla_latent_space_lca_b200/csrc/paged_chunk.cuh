@@ -53,6 +53,11 @@ constexpr int PC_KWARPS = 3, PC_VWARPS = 2;      // fetch: warps 4 .. 6 for S, 7
 constexpr int PC_WARP_S = 9, PC_WARP_PV = 10;    // MMA issue (CTA 0)
 constexpr int PC_THREADS = 32 * 11;
 constexpr int PC_MAX_CLUSTERS = 80;              // partial outputs: two per cluster
+constexpr int PC_PLAN_BATCH = 1024;              // sequences that the plan keeps in shared memory
+// A sequence with fewer query tiles than this comes from memory rather than
+// from L2: its rows are asked for this many cache tiles ahead of their copies
+// (the ring alone has 56 KB under way per SM, 3.5 TB/s at the latency under load).
+constexpr int PC_AHEAD_SHARERS = 4, PC_AHEAD = 3;
 constexpr int PC_OVER = 2;                       // cost of a piece beyond its tiles, in tiles
 
 // A query tile: tokens t0 .. t0 + live - 1 of sequence b; token t attends
@@ -60,16 +65,24 @@ constexpr int PC_OVER = 2;                       // cost of a piece beyond its t
 // end to end in units of one cache tile, PC_OVER more for each query tile,
 // and cut into one equal range per cluster.
 struct alignas(16) ChunkTile {
-    int32_t b, t0, live, tiles;
+    int32_t b, t0;
+    int16_t live, sharers;   // sharers: query tiles of the sequence (at most 32767)
+    int32_t tiles;
     int64_t row_base, unit0;
 };
 
+// A query tile that a cluster's border cuts: pieces by the clusters c0 .. c1.
+struct alignas(16) ChunkMerge {
+    int32_t t0, live, c0, c1;
+};
+
 struct ChunkPlan {
-    int32_t *q0, *q1;        // [B] rows of the batch, clamped and disjoint
+    int32_t *q0, *q1;        // [B] rows of the batch, clamped and disjoint (batches above PC_PLAN_BATCH)
     int32_t *tile0;          // [B] first query tile
     ChunkTile *tile;         // [T / 8 + B + 1]; tile[nq].unit0: all units
     int32_t *first;          // [PC_MAX_CLUSTERS] query tile of the cluster's first unit
     int32_t *nq;             // [1] query tiles
+    ChunkMerge *merge;       // [PC_MAX_CLUSTERS] by the first border inside; c1 < 0: none
 };
 
 struct ChunkArgs {
@@ -133,7 +146,7 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
 {
     __shared__ BlockScan sc;
     __shared__ BlockScan64 sc64;
-    __shared__ int32_t wmax[32], run_max;
+    __shared__ int32_t wmax[32], run_max, sq0[PC_PLAN_BATCH], sq1[PC_PLAN_BATCH], st0[PC_PLAN_BATCH];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         run_max = 0;
@@ -145,6 +158,8 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
     griddep_launch_dependents();
     const int64_t max_rows = a.max_blocks << a.page_shift;
     const ChunkPlan &p = a.plan;
+    const bool small = a.B <= PC_PLAN_BATCH;
+    int32_t *q0s = small ? sq0 : p.q0, *q1s = small ? sq1 : p.q1, *tile0 = small ? st0 : p.tile0;
     for (int base = 0; base < a.B; base += int(blockDim.x)) {
         const int b = base + int(threadIdx.x);
         int32_t lo = 0, hi = 0;
@@ -178,9 +193,9 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
         const int32_t q0 = m, q1 = max(hi, m);
         const int32_t t0 = block_scan(b < a.B ? (q1 - q0 + PC_TOKENS - 1) / PC_TOKENS : 0, 0x3fffffff, sc);
         if (b < a.B) {
-            p.q0[b] = q0;
-            p.q1[b] = q1;
-            p.tile0[b] = t0;
+            q0s[b] = q0;
+            q1s[b] = q1;
+            tile0[b] = t0;
         }
     }
     __syncthreads();   // every sequence's entries are written
@@ -189,11 +204,12 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
         const int i = base + int(threadIdx.x);
         ChunkTile w{};
         if (i < nq) {
-            w.b = last_le(p.tile0, a.B, i);
-            const int32_t q1 = p.q1[w.b];
+            w.b = last_le(tile0, a.B, i);
+            const int32_t q0 = q0s[w.b], q1 = q1s[w.b];
             // the tiles with the most rows first
-            w.t0 = p.q0[w.b] + PC_TOKENS * ((q1 - p.q0[w.b] + PC_TOKENS - 1) / PC_TOKENS - 1 - (i - p.tile0[w.b]));
-            w.live = min(PC_TOKENS, q1 - w.t0);
+            w.t0 = q0 + PC_TOKENS * ((q1 - q0 + PC_TOKENS - 1) / PC_TOKENS - 1 - (i - tile0[w.b]));
+            w.live = int16_t(min(PC_TOKENS, q1 - w.t0));
+            w.sharers = int16_t(min((q1 - q0 + PC_TOKENS - 1) / PC_TOKENS, 32767));
             w.row_base = int64_t(a.seq_lens[w.b]) - a.q_start[w.b + 1] + 1;
             w.tiles = (int64_t(clamp_rows(w.row_base + w.t0 + w.live - 1, max_rows)) + PC_TILE - 1) / PC_TILE;
         }
@@ -201,6 +217,7 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
         if (i < nq) p.tile[i] = w;
     }
     const int64_t units = sc64.carry;
+    for (int c = threadIdx.x; c < clusters; c += int(blockDim.x)) p.merge[c].c1 = -1;
     if (threadIdx.x == 0) {
         p.tile[nq].unit0 = units;
         *p.nq = nq;
@@ -209,8 +226,17 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
     // cluster c starts at unit c * units / clusters
     for (int i = threadIdx.x; i < nq; i += int(blockDim.x)) {
         const int64_t u0 = p.tile[i].unit0, u1 = p.tile[i + 1].unit0;
-        for (int64_t c = (u0 * clusters + units - 1) / units; c < clusters && split_begin(int(c), units, clusters) < u1; ++c)
+        int32_t c0 = -1, c1 = -1;   // first and last border strictly inside the tile's cache tiles
+        for (int64_t c = (u0 * clusters + units - 1) / units; c < clusters; ++c) {
+            const int64_t at = split_begin(int(c), units, clusters);
+            if (at >= u1) break;
             p.first[c] = i;
+            if (at > u0 + PC_OVER) {
+                if (c0 < 0) c0 = int32_t(c);
+                c1 = int32_t(c);
+            }
+        }
+        if (c0 >= 0) p.merge[c0] = ChunkMerge{p.tile[i].t0, p.tile[i].live, c0 - 1, c1};
     }
 }
 
@@ -426,6 +452,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
+// The box into L2 only.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int x, int y, int z, int w)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
 // 32-byte store of eight 32-bit values.
 __device__ __forceinline__ void st_global_32b(void *p, const uint32_t (&v)[8])
 {
@@ -482,7 +517,8 @@ struct ChunkRange {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const ChunkArgs a)
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_rows,
+                       const ChunkArgs a)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -515,10 +551,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     const uint32_t drain_s = BAR(B0 + 11), drain_pv = BAR(B0 + 12);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + PC_OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + PC_OFF_MISC + 4);
+    volatile int *progress = reinterpret_cast<volatile int *>(smem + PC_OFF_MISC + 8);   // tiles that S's copies have reached
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < PC_BARS; ++i) mbar_init(BAR(i), i < B0 + 5 ? 1 : i <= B0 + 9 ? 2 * PC_SOFTMAX : 1);
         *abort_flag = 0;
+        *progress = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -597,6 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             for (int c = 0; c < LOOKUPS; ++c) page[c] = !K || c * sub < 64 ? page_of(row0 + c * sub) : -1;
             const int last = w.v_slots(w.n() - 1, max_rows);
             for (int i = w.n(); i > 0 && ok; --i, ++n, row0 += PC_TILE) {
+                if (K && p == 0) *progress = int(n);
 #pragma unroll
                 for (int c = 0; c < LOOKUPS; ++c) group[c] = group_of(page[c], row0 + c * sub);
 #pragma unroll
@@ -637,6 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 }
             }
         }
+        if (K && p == 0) *progress = 0x7fffffff;
         // No copy left in flight, and every commit that arrives at this CTA
         // has: this producer's among the ring's last uses, backwards.
         while (ok && x >= STEP && x - STEP + RING >= base) {
@@ -661,7 +701,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     } else if (warp >= PC_SOFTMAX + PC_KWARPS && warp < PC_WARP_S) {
         if (lane == 0) produce(std::false_type{}, uint32_t(warp - PC_SOFTMAX - PC_KWARPS));
         __syncwarp();
-    } else if (warp == PC_WARP_S && cta == 0) {
+    } else if (warp == PC_WARP_S && cta == 1) {
+        // ------------------------------------------------------------ L2 ahead of the copies
+        // (nothing waits for this warp, and it may fall behind: it only ever
+        // skips what the copies have passed)
+        const int box_shift = min(a.page_shift, 6);
+        int n = 0;
+        while (range.next(a.plan, w)) {
+            const int m = w.n();
+            if (w.t.sharers < PC_AHEAD_SHARERS) {
+                const int32_t *table = a.block_table + size_t(w.t.b) * size_t(a.max_blocks);
+                for (int i = 0; i < m; ++i) {
+                    int reached;
+                    for (int it = 0; (reached = *progress) < n + i - PC_AHEAD && it < 100000; ++it) __nanosleep(100);
+                    if (__shfl_sync(0xffffffffu, reached, 0) > n + i) continue;
+                    const int r = (w.k0 + i) * PC_TILE + (lane << box_shift);
+                    const int k = r >> a.page_shift;
+                    if (lane < (PC_TILE >> box_shift) && k < int(a.max_blocks)) {
+                        const int32_t page = __ldg(table + k);
+                        if (uint32_t(page) < uint32_t(a.n_pages))
+                            tma_prefetch_4d(&map_rows, 0, 0, 0,
+                                            (page << (a.page_shift - 3)) + ((r & ((1 << a.page_shift) - 1)) >> 3));
+                    }
+                    __syncwarp();
+                }
+            }
+            n += m;
+        }
+    } else if (warp == PC_WARP_S) {
         // ------------------------------------------------------------ S = Q . tile^T for the pair
         constexpr uint32_t IDESC_S = idesc_bf16(PC_ROWS, PC_TILE, 0, 0);
         const uint64_t q_desc = sdesc_sw128(sbase, 16, 1024), k_desc = sdesc_sw128(kaddr(0), 16, 1024);
@@ -1004,64 +1071,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
 // ------------------------------------------------------------ merge
 // Query tiles cut by a cluster's border: o = sum_s 2^(m_s - M) O_s /
 // sum_s 2^(m_s - M) l_s per query row, one warp each (lane: 16 columns),
-// written as hi + lo.  blockIdx.y + 1 is the first cluster border inside the
-// query tile.
-constexpr int MG_THREADS = 256;
+// written as hi + lo.  blockIdx.y + 1 is the first border inside the query
+// tile, which starts in cluster c0 = blockIdx.y and has pieces of all clusters
+// to c1 (a range between equal borders holds none).
+constexpr int MG_THREADS = 512, MG_ROWS = 2;   // query rows per warp
 
 __global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs a, int clusters)
 {
     griddep_wait();
     griddep_launch_dependents();
     const ChunkPlan &p = a.plan;
-    const int c = int(blockIdx.y) + 1, lane = threadIdx.x & 31;
-    const int r = int(blockIdx.x) * (MG_THREADS / 32) + int(threadIdx.x >> 5);   // query row
-    const int32_t nq = *p.nq;
-    if (nq == 0) return;
-    const int64_t units = p.tile[nq].unit0;
-    const int64_t at = split_begin(c, units, clusters);
-    if (at >= units) return;
-    const ChunkTile t = p.tile[p.first[c]];
-    const int64_t u = t.unit0 + PC_OVER;
-    if (at - u <= 0 || at - u >= t.tiles || split_begin(c - 1, units, clusters) - u > 0) return;
-    if (r / LCA_HEADS >= t.live) return;
-    int last = c;   // the cluster that holds the query tile's last cache tile
-    while (last + 1 < clusters && split_begin(last + 1, units, clusters) - u < t.tiles) ++last;
-    // cluster c - 1 holds the first piece; a range between equal borders holds none
-    const auto none = [&](int k) { return split_begin(k, units, clusters) == split_begin(k + 1, units, clusters); };
-    const auto slot = [&](int k) { return size_t(k == c - 1 ? 2 * k + 1 : 2 * k) * PC_ROWS + r; };
-    float M = -1e30f;
-    for (int k = c - 1; k <= last; ++k)
-        if (!none(k)) M = fmaxf(M, a.part_ml[slot(k) * 2]);
-    float den = 0.f, acc[16];
+    const int lane = threadIdx.x & 31;
+    const ChunkMerge mg = p.merge[blockIdx.y + 1];
+    if (mg.c1 < 0) return;
+    const int64_t units = p.tile[*p.nq].unit0;
+#pragma unroll 1
+    for (int y = 0; y < MG_ROWS; ++y) {
+        const int r = (int(blockIdx.x) * (MG_THREADS / 32) + int(threadIdx.x >> 5)) * MG_ROWS + y;   // query row
+        if (r / LCA_HEADS >= mg.live) return;
+        const auto slot = [&](int k) { return size_t(k == mg.c0 ? 2 * k + 1 : 2 * k) * PC_ROWS + r; };
+        float M = -1e30f, den = 0.f, acc[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-    for (int k = c - 1; k <= last; ++k) {
-        if (none(k)) continue;
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(k) * 2);
-        if (ml.y == 0.f) continue;   // nothing attended in this piece
-        const float f = fast_exp2(ml.x - M);
-        den = fmaf(f, ml.y, den);
-        const float4 *o = reinterpret_cast<const float4 *>(a.part_o + slot(k) * LCA_DC + 16 * lane);
+        for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+        // 32 pieces at a time, a lane each: maximum, weight, sum; then all lanes the values
+        for (int k0 = mg.c0; k0 <= mg.c1; k0 += 32) {
+            const int k = k0 + lane;
+            float2 ml = make_float2(-1e30f, 0.f);
+            if (k <= mg.c1 && split_begin(k, units, clusters) < split_begin(k + 1, units, clusters))
+                ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(k) * 2);
+            float top = ml.x;
+#pragma unroll
+            for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            top = fmaxf(top, M);
+            const float old = fast_exp2(M - top);
+            M = top;
+            // a piece in which nothing is attended has weight 0, whatever its O
+            const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);
+            float sum = f * ml.y;
+#pragma unroll
+            for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            den = fmaf(den, old, sum);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] *= old;
+            const int n = min(32, mg.c1 - k0 + 1);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                if (fi == 0.f) continue;
+                const float4 *o = reinterpret_cast<const float4 *>(a.part_o + slot(k0 + i) * LCA_DC) + lane;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {   // columns 128 v + 4 lane ..
+                    const float4 x = o[32 * v];
+                    acc[4 * v] = fmaf(fi, x.x, acc[4 * v]);
+                    acc[4 * v + 1] = fmaf(fi, x.y, acc[4 * v + 1]);
+                    acc[4 * v + 2] = fmaf(fi, x.z, acc[4 * v + 2]);
+                    acc[4 * v + 3] = fmaf(fi, x.w, acc[4 * v + 3]);
+                }
+            }
+        }
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        uint16_t *hl = a.o_hl + (size_t(mg.t0 + r / LCA_HEADS) * LCA_HEADS + r % LCA_HEADS) * (2 * LCA_DC) + 4 * lane;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            const float4 x = o[v];
-            acc[4 * v] = fmaf(f, x.x, acc[4 * v]);
-            acc[4 * v + 1] = fmaf(f, x.y, acc[4 * v + 1]);
-            acc[4 * v + 2] = fmaf(f, x.z, acc[4 * v + 2]);
-            acc[4 * v + 3] = fmaf(f, x.w, acc[4 * v + 3]);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float o0 = acc[4 * v + 2 * e] * inv, o1 = acc[4 * v + 2 * e + 1] * inv;
+                hi[e] = pack_bf16(o0, o1);
+                lo[e] = pack_bf16(o0 - bf_lo(hi[e]), o1 - bf_hi(hi[e]));
+            }
+            *reinterpret_cast<uint2 *>(hl + 128 * v) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(hl + LCA_DC + 128 * v) = make_uint2(lo[0], lo[1]);
         }
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float o0 = acc[2 * e] * inv, o1 = acc[2 * e + 1] * inv;
-        hi[e] = pack_bf16(o0, o1);
-        lo[e] = pack_bf16(o0 - bf_lo(hi[e]), o1 - bf_hi(hi[e]));
-    }
-    uint16_t *hl = a.o_hl + (size_t(t.t0 + r / LCA_HEADS) * LCA_HEADS + r % LCA_HEADS) * (2 * LCA_DC) + 16 * lane;
-    st_global_32b(hl, hi);
-    st_global_32b(hl + LCA_DC, lo);
 }
 
 }  // namespace lca

@@ -6,11 +6,6 @@
 // B = W_UV[h] ([512][128], TMA boxes {64, 64, 1}, N-contiguous = MN-major),
 // K = 512 in 8 chunks of 64 through a 4-stage TMA ring.  Rows past R are
 // zero-filled by TMA and never stored.
-//
-// PAGED: A holds o as two bf16 values per element, [R][16][hi 512 | lo 512]
-// (K = 1024 against W_UV twice: o enters the product to 2^-16, and the only
-// rounding to bf16 left is the result's), out is bf16, and only rows
-// q_start[0] .. q_start[B]-1 are stored.
 #pragma once
 #include "common.cuh"
 
@@ -25,11 +20,9 @@ constexpr int GM_SMEM = GM_OFF_BAR + 256;
 constexpr int GM_SMEM_ALLOC = GM_SMEM + 1024;
 constexpr uint32_t GM_TM_COLS = 128;
 
-template <bool PAGED = false>
 __global__ void __launch_bounds__(128, 1)
     wuv_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                    float *__restrict__ out, int64_t R, uint16_t *__restrict__ out16 = nullptr,
-                    const int32_t *__restrict__ q_start = nullptr, int B = 0)
+                    float *__restrict__ out, int64_t R)
 {
     extern __shared__ uint8_t gm_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -63,15 +56,7 @@ __global__ void __launch_bounds__(128, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    constexpr int KB = LCA_DC / 64;                 // 8 k-chunks of W_UV
-    constexpr int KC = PAGED ? 2 * KB : KB;         // of A
-    int64_t row0 = 0, row1 = R;
-    if constexpr (PAGED) {
-        griddep_wait();   // o comes from the kernel before
-        griddep_launch_dependents();
-        row0 = q_start[0];
-        row1 = min64(R, q_start[B]);
-    }
+    constexpr int KC = LCA_DC / 64;   // 8 k-chunks
 
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&map_a);
@@ -84,8 +69,8 @@ __global__ void __launch_bounds__(128, 1)
             mbar_expect_tx(full(s), GM_STAGE);
             const uint32_t st = sbase + s * GM_STAGE;
             tma_load_3d(st, &map_a, full(s), 64 * kc, h, mt * 128, pa);
-            tma_load_3d(st + GM_A, &map_b, full(s), 0, 64 * (kc % KB), h, pb);
-            tma_load_3d(st + GM_A + 8192, &map_b, full(s), 64, 64 * (kc % KB), h, pb);
+            tma_load_3d(st + GM_A, &map_b, full(s), 0, 64 * kc, h, pb);
+            tma_load_3d(st + GM_A + 8192, &map_b, full(s), 64, 64 * kc, h, pb);
             last[s] = kc;
         }
         for (int s = 0; s < GM_STAGES; ++s)
@@ -123,15 +108,7 @@ __global__ void __launch_bounds__(128, 1)
         for (int cc = 0; cc < 4; ++cc) {
             float v[32];
             tmem_ld32(ta + 32 * cc, v);
-            if constexpr (PAGED) {
-                if (row >= row0 && row < row1) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(out16 + (size_t(row) * LCA_HEADS + h) * LCA_DV + 32 * cc);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dst[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
-                                            pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
-                }
-            } else if (row < R) {
+            if (row < R) {
                 float4 *dst = reinterpret_cast<float4 *>(out + (size_t(row) * LCA_HEADS + h) * LCA_DV + 32 * cc);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
