@@ -619,12 +619,11 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
     a.part_o = w.part_o;
     a.part_ml = w.part_ml;
     const int clusters = std::min(std::max(1, dev->sms / 2), PC_MAX_CLUSTERS);
-    CUtensorMap map_q, map_k, map_v, map_rows, map_a, map_w;
+    CUtensorMap map_q, map_k, map_v, map_a, map_w;
     const uint64_t rows = uint64_t(c.n_pages) << c.shift, q_rows = uint64_t(c.T) * LCA_HEADS;
     if ((rc = make_map_rows(&map_q, c.q, q_rows, 1, q_rows, 64)) ||
         (rc = make_map_pages(&map_k, c.pages, rows, std::min(1 << c.shift, 64), 1)) ||
         (rc = make_map_pages(&map_v, c.pages, rows, 16, 4)) ||
-        (rc = make_map_pages(&map_rows, c.pages, rows, std::min(1 << c.shift, 64), LCA_D / 64)) ||
         (rc = make_map3(&map_a, w.o_hl, 2 * LCA_DC, LCA_HEADS, uint64_t(c.T), uint64_t(LCA_DC) * 4,
                         uint64_t(LCA_HEADS) * LCA_DC * 4, 64, 1, 128)) ||
         (rc = make_map3(&map_w, c.w_uv, LCA_DV, LCA_DC, LCA_HEADS, LCA_DV * 2, LCA_DC * LCA_DV * 2, 64, 64, 1)))
@@ -637,12 +636,12 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
     {
         Launch l(c.st, K_CHUNK);
         const cudaError_t e = launch_ex(paged_chunk_kernel, dim3(2 * clusters), dim3(PC_THREADS), PC_SMEM_ALLOC, c.st,
-                                        true, map_q, map_k, map_v, map_rows, a);
+                                        true, map_q, map_k, map_v, a);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     if (clusters > 1) {
         Launch l(c.st, K_MERGE);
-        const cudaError_t e = launch_ex(paged_merge_kernel, dim3(PC_ROWS * 32 / MG_THREADS / MG_ROWS, clusters - 1),
+        const cudaError_t e = launch_ex(paged_merge_kernel, dim3(PC_ROWS * 32 / MG_THREADS, clusters - 1),
                                         dim3(MG_THREADS), 0, c.st, true, a, clusters);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }

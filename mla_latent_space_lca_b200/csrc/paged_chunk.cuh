@@ -35,11 +35,11 @@ constexpr int PC_TILE = 128;                     // cache rows per tile
 constexpr int PC_Q = 9 * 8192;                   // 64 query rows, nine [64 x 64] blocks
 constexpr int PC_SLOT = 8192;
 constexpr int PC_KS = 9, PC_VS = 8;              // slots of a tile: for S, for PV
-constexpr int PC_KRING = 7, PC_VRING = 8;        // (a tile's PV slots fit the ring: see vready)
+constexpr int PC_KRING = 9, PC_VRING = 8;        // (a tile's PV slots fit the ring: see vready)
 constexpr int PC_SLOTS = PC_KRING + PC_VRING;
 constexpr int PC_P = 2 * 8192;                   // P [64 x 128] bf16, two [64 x 64] blocks
 constexpr int PC_OFF_P = PC_Q;
-constexpr int PC_OFF_RING = PC_OFF_P + 2 * PC_P;
+constexpr int PC_OFF_RING = PC_OFF_P + PC_P;
 constexpr int PC_OFF_X = PC_OFF_RING + PC_SLOTS * PC_SLOT;   // [2][128] row maxima or sums
 constexpr int PC_OFF_BAR = PC_OFF_X + 2 * 128 * 4;
 constexpr int PC_BARS = 2 * PC_SLOTS + 13;
@@ -54,10 +54,6 @@ constexpr int PC_WARP_S = 9, PC_WARP_PV = 10;    // MMA issue (CTA 0)
 constexpr int PC_THREADS = 32 * 11;
 constexpr int PC_MAX_CLUSTERS = 80;              // partial outputs: two per cluster
 constexpr int PC_PLAN_BATCH = 1024;              // sequences that the plan keeps in shared memory
-// A sequence with fewer query tiles than this comes from memory rather than
-// from L2: its rows are asked for this many cache tiles ahead of their copies
-// (the ring alone has 56 KB under way per SM, 3.5 TB/s at the latency under load).
-constexpr int PC_AHEAD_SHARERS = 4, PC_AHEAD = 3;
 constexpr int PC_OVER = 2;                       // cost of a piece beyond its tiles, in tiles
 
 // A query tile: tokens t0 .. t0 + live - 1 of sequence b; token t attends
@@ -65,9 +61,7 @@ constexpr int PC_OVER = 2;                       // cost of a piece beyond its t
 // end to end in units of one cache tile, PC_OVER more for each query tile,
 // and cut into one equal range per cluster.
 struct alignas(16) ChunkTile {
-    int32_t b, t0;
-    int16_t live, sharers;   // sharers: query tiles of the sequence (at most 32767)
-    int32_t tiles;
+    int32_t b, t0, live, tiles;
     int64_t row_base, unit0;
 };
 
@@ -208,8 +202,7 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
             const int32_t q0 = q0s[w.b], q1 = q1s[w.b];
             // the tiles with the most rows first
             w.t0 = q0 + PC_TOKENS * ((q1 - q0 + PC_TOKENS - 1) / PC_TOKENS - 1 - (i - tile0[w.b]));
-            w.live = int16_t(min(PC_TOKENS, q1 - w.t0));
-            w.sharers = int16_t(min((q1 - q0 + PC_TOKENS - 1) / PC_TOKENS, 32767));
+            w.live = min(PC_TOKENS, q1 - w.t0);
             w.row_base = int64_t(a.seq_lens[w.b]) - a.q_start[w.b + 1] + 1;
             w.tiles = (int64_t(clamp_rows(w.row_base + w.t0 + w.live - 1, max_rows)) + PC_TILE - 1) / PC_TILE;
         }
@@ -217,26 +210,36 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
         if (i < nq) p.tile[i] = w;
     }
     const int64_t units = sc64.carry;
-    for (int c = threadIdx.x; c < clusters; c += int(blockDim.x)) p.merge[c].c1 = -1;
     if (threadIdx.x == 0) {
         p.tile[nq].unit0 = units;
         *p.nq = nq;
     }
     __syncthreads();
-    // cluster c starts at unit c * units / clusters
-    for (int i = threadIdx.x; i < nq; i += int(blockDim.x)) {
-        const int64_t u0 = p.tile[i].unit0, u1 = p.tile[i + 1].unit0;
-        int32_t c0 = -1, c1 = -1;   // first and last border strictly inside the tile's cache tiles
-        for (int64_t c = (u0 * clusters + units - 1) / units; c < clusters; ++c) {
-            const int64_t at = split_begin(int(c), units, clusters);
-            if (at >= u1) break;
-            p.first[c] = i;
-            if (at > u0 + PC_OVER) {
-                if (c0 < 0) c0 = int32_t(c);
-                c1 = int32_t(c);
-            }
+    // Cluster c starts at unit c * units / clusters: its query tile, and whether
+    // that border cuts the tile's cache tiles.
+    __shared__ int32_t at_tile[PC_MAX_CLUSTERS];
+    __shared__ bool cuts[PC_MAX_CLUSTERS];
+    const int c = threadIdx.x;
+    if (c < clusters && nq > 0) {
+        const int64_t at = split_begin(c, units, clusters);
+        int lo = 0, hi = nq - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.tile[mid].unit0 <= at) lo = mid;
+            else hi = mid - 1;
         }
-        if (c0 >= 0) p.merge[c0] = ChunkMerge{p.tile[i].t0, p.tile[i].live, c0 - 1, c1};
+        p.first[c] = lo;
+        at_tile[c] = lo;
+        cuts[c] = at < units && at > p.tile[lo].unit0 + PC_OVER;
+    }
+    __syncthreads();
+    if (c < clusters) {
+        ChunkMerge g{0, 0, 0, -1};
+        if (nq > 0 && c > 0 && cuts[c] && !(cuts[c - 1] && at_tile[c - 1] == at_tile[c])) {
+            g = ChunkMerge{p.tile[at_tile[c]].t0, p.tile[at_tile[c]].live, c - 1, c};
+            while (g.c1 + 1 < clusters && cuts[g.c1 + 1] && at_tile[g.c1 + 1] == at_tile[c]) ++g.c1;
+        }
+        p.merge[c] = g;
     }
 }
 
@@ -452,15 +455,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
-// The box into L2 only.
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int x, int y, int z, int w)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
-}
-
 // 32-byte store of eight 32-bit values.
 __device__ __forceinline__ void st_global_32b(void *p, const uint32_t (&v)[8])
 {
@@ -517,8 +511,7 @@ struct ChunkRange {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_rows,
-                       const ChunkArgs a)
+                       const __grid_constant__ CUtensorMap map_v, const ChunkArgs a)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -551,12 +544,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     const uint32_t drain_s = BAR(B0 + 11), drain_pv = BAR(B0 + 12);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + PC_OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + PC_OFF_MISC + 4);
-    volatile int *progress = reinterpret_cast<volatile int *>(smem + PC_OFF_MISC + 8);   // tiles that S's copies have reached
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < PC_BARS; ++i) mbar_init(BAR(i), i < B0 + 5 ? 1 : i <= B0 + 9 ? 2 * PC_SOFTMAX : 1);
         *abort_flag = 0;
-        *progress = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -635,7 +626,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             for (int c = 0; c < LOOKUPS; ++c) page[c] = !K || c * sub < 64 ? page_of(row0 + c * sub) : -1;
             const int last = w.v_slots(w.n() - 1, max_rows);
             for (int i = w.n(); i > 0 && ok; --i, ++n, row0 += PC_TILE) {
-                if (K && p == 0) *progress = int(n);
 #pragma unroll
                 for (int c = 0; c < LOOKUPS; ++c) group[c] = group_of(page[c], row0 + c * sub);
 #pragma unroll
@@ -676,7 +666,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 }
             }
         }
-        if (K && p == 0) *progress = 0x7fffffff;
         // No copy left in flight, and every commit that arrives at this CTA
         // has: this producer's among the ring's last uses, backwards.
         while (ok && x >= STEP && x - STEP + RING >= base) {
@@ -701,34 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     } else if (warp >= PC_SOFTMAX + PC_KWARPS && warp < PC_WARP_S) {
         if (lane == 0) produce(std::false_type{}, uint32_t(warp - PC_SOFTMAX - PC_KWARPS));
         __syncwarp();
-    } else if (warp == PC_WARP_S && cta == 1) {
-        // ------------------------------------------------------------ L2 ahead of the copies
-        // (nothing waits for this warp, and it may fall behind: it only ever
-        // skips what the copies have passed)
-        const int box_shift = min(a.page_shift, 6);
-        int n = 0;
-        while (range.next(a.plan, w)) {
-            const int m = w.n();
-            if (w.t.sharers < PC_AHEAD_SHARERS) {
-                const int32_t *table = a.block_table + size_t(w.t.b) * size_t(a.max_blocks);
-                for (int i = 0; i < m; ++i) {
-                    int reached;
-                    for (int it = 0; (reached = *progress) < n + i - PC_AHEAD && it < 100000; ++it) __nanosleep(100);
-                    if (__shfl_sync(0xffffffffu, reached, 0) > n + i) continue;
-                    const int r = (w.k0 + i) * PC_TILE + (lane << box_shift);
-                    const int k = r >> a.page_shift;
-                    if (lane < (PC_TILE >> box_shift) && k < int(a.max_blocks)) {
-                        const int32_t page = __ldg(table + k);
-                        if (uint32_t(page) < uint32_t(a.n_pages))
-                            tma_prefetch_4d(&map_rows, 0, 0, 0,
-                                            (page << (a.page_shift - 3)) + ((r & ((1 << a.page_shift) - 1)) >> 3));
-                    }
-                    __syncwarp();
-                }
-            }
-            n += m;
-        }
-    } else if (warp == PC_WARP_S) {
+    } else if (warp == PC_WARP_S && cta == 0) {
         // ------------------------------------------------------------ S = Q . tile^T for the pair
         constexpr uint32_t IDESC_S = idesc_bf16(PC_ROWS, PC_TILE, 0, 0);
         const uint64_t q_desc = sdesc_sw128(sbase, 16, 1024), k_desc = sdesc_sw128(kaddr(0), 16, 1024);
@@ -787,10 +749,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
         constexpr uint32_t IDESC_PV = idesc_bf16(PC_ROWS, 256, 0, 1);
         const uint64_t p_desc = sdesc_sw128(sbase + PC_OFF_P, 16, 1024), v_desc = sdesc_sw128(vaddr(0), 1024, 4096);
         // 16-row parts v .. v + count - 1 of a tile, from slot `at` on
-        const auto pv_mmas = [&](RingPlace<PC_VRING> at, uint64_t pd, int v, int count, bool add) {
+        const auto pv_mmas = [&](RingPlace<PC_VRING> at, int v, int count, bool add) {
 #pragma unroll 1
             for (; count > 0; --count, ++v, ++at) {
-                const uint64_t p = pd + uint64_t((v >> 2) * (8192 >> 4) + (v & 3) * 2);
+                const uint64_t p = p_desc + uint64_t((v >> 2) * (8192 >> 4) + (v & 3) * 2);
                 const uint64_t vd = v_desc + uint64_t(at.slot * (PC_SLOT >> 4));
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -818,19 +780,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 }
                 if (i == 0 && !(ok = warp_wait(oread, (pieces & 1) ^ 1, abort_flag, 12))) break;
                 if (!(ok = warp_wait(pfull(n), (n >> 1) & 1, abort_flag, 13))) break;
-                const uint64_t pd = p_desc + (n & 1) * (PC_P >> 4);
                 bool looked = at.look(vfull(0), 0, lane);
                 for (int v = 0; v < nvs;) {
                     const int got = min(at.count(vfull(0), looked, abort_flag, 14), nvs - v);
                     if (!(ok = got > 0)) break;
                     tc_fence_after();
-                    if (got > 1 && elect_one()) pv_mmas(at, pd, v, got - 1, i > 0);
+                    if (got > 1 && elect_one()) pv_mmas(at, v, got - 1, i > 0);
                     __syncwarp();
                     v += got - 1;
                     at.skip(uint32_t(got - 1));
                     looked = at.look(vfull(0), 1, lane);
                     if (elect_one()) {
-                        pv_mmas(at, pd, v, 1, i > 0);
+                        pv_mmas(at, v, 1, i > 0);
                         if (v + 1 == nvs) tc_commit_pair(vdone(n));
                     }
                     __syncwarp();
@@ -963,32 +924,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     m = tmax;
                     l *= f;
                 }
-                // P(n - 2) has been used
-                ok = ok && warp_wait(vdone(n), ((n >> 1) & 1) ^ 1, abort_flag, 17);
-                uint8_t *prow = smem + PC_OFF_P + (n & 1) * PC_P + half * 8192 + (row >> 3) * 1024 + (row & 7) * 128;
                 const uint64_t scale = pack2(a.sl2, a.sl2), shift = pack2(-m, -m);
                 uint64_t sum[2] = {0, 0};
+                uint32_t pk[32];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    uint32_t v[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        float p0, p1;
-                        unpack2(fma2(pack2(s[8 * e + 2 * x], s[8 * e + 2 * x + 1]), scale, shift), p0, p1);
-                        p0 = fast_exp2(p0);
-                        p1 = fast_exp2(p1);
-                        sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
-                        v[x] = pack_bf16(p0, p1);
-                    }
-                    *reinterpret_cast<uint4 *>(prow + ((e ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                for (int x = 0; x < 32; ++x) {
+                    float p0, p1;
+                    unpack2(fma2(pack2(s[2 * x], s[2 * x + 1]), scale, shift), p0, p1);
+                    p0 = fast_exp2(p0);
+                    p1 = fast_exp2(p1);
+                    sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
+                    pk[x] = pack_bf16(p0, p1);
                 }
                 float sum0, sum1;
                 unpack2(add2(sum[0], sum[1]), sum0, sum1);
                 l += sum0 + sum1;
+                // P(n - 1) has been used, and O holds PV(n - 1)
+                if (n > 0) ok = ok && warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 17);
+                uint8_t *prow = smem + PC_OFF_P + half * 8192 + (row >> 3) * 1024 + (row & 7) * 128;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<uint4 *>(prow + ((e ^ (row & 7)) << 4)) =
+                        make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                 fence_proxy_async();
                 if (__any_sync(0xffffffffu, f != 1.f)) {
-                    // O must hold PV(n - 1) before it is rescaled
-                    ok = ok && warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 18);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 8; ++c) {
@@ -1074,7 +1033,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
 // written as hi + lo.  blockIdx.y + 1 is the first border inside the query
 // tile, which starts in cluster c0 = blockIdx.y and has pieces of all clusters
 // to c1 (a range between equal borders holds none).
-constexpr int MG_THREADS = 512, MG_ROWS = 2;   // query rows per warp
+constexpr int MG_THREADS = 256;
 
 __global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs a, int clusters)
 {
@@ -1082,67 +1041,72 @@ __global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs
     griddep_launch_dependents();
     const ChunkPlan &p = a.plan;
     const int lane = threadIdx.x & 31;
+    const int r = int(blockIdx.x) * (MG_THREADS / 32) + int(threadIdx.x >> 5);   // query row
     const ChunkMerge mg = p.merge[blockIdx.y + 1];
-    if (mg.c1 < 0) return;
+    if (mg.c1 < 0 || r / LCA_HEADS >= mg.live) return;
     const int64_t units = p.tile[*p.nq].unit0;
-#pragma unroll 1
-    for (int y = 0; y < MG_ROWS; ++y) {
-        const int r = (int(blockIdx.x) * (MG_THREADS / 32) + int(threadIdx.x >> 5)) * MG_ROWS + y;   // query row
-        if (r / LCA_HEADS >= mg.live) return;
-        const auto slot = [&](int k) { return size_t(k == mg.c0 ? 2 * k + 1 : 2 * k) * PC_ROWS + r; };
-        float M = -1e30f, den = 0.f, acc[16];
+    const auto slot = [&](int k) { return size_t(k == mg.c0 ? 2 * k + 1 : 2 * k) * PC_ROWS + r; };
+    float M = -1e30f, den = 0.f, acc[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-        // 32 pieces at a time, a lane each: maximum, weight, sum; then all lanes the values
-        for (int k0 = mg.c0; k0 <= mg.c1; k0 += 32) {
-            const int k = k0 + lane;
-            float2 ml = make_float2(-1e30f, 0.f);
-            if (k <= mg.c1 && split_begin(k, units, clusters) < split_begin(k + 1, units, clusters))
-                ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(k) * 2);
-            float top = ml.x;
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    // 32 pieces at a time, a lane each: maximum, weight, sum; then all lanes the values
+    for (int k0 = mg.c0; k0 <= mg.c1; k0 += 32) {
+        const int k = k0 + lane;
+        float2 ml = make_float2(-1e30f, 0.f);
+        // (fewer units than clusters: ranges without any)
+        if (k <= mg.c1 && (units >= clusters || split_begin(k, units, clusters) < split_begin(k + 1, units, clusters)))
+            ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(k) * 2);
+        float top = ml.x;
 #pragma unroll
-            for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            top = fmaxf(top, M);
-            const float old = fast_exp2(M - top);
-            M = top;
-            // a piece in which nothing is attended has weight 0, whatever its O
-            const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);
-            float sum = f * ml.y;
+        for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = fmaxf(top, M);
+        const float old = fast_exp2(M - top);
+        M = top;
+        // a piece in which nothing is attended has weight 0, whatever its O
+        const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);
+        float sum = f * ml.y;
 #pragma unroll
-            for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            den = fmaf(den, old, sum);
+        for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        den = fmaf(den, old, sum);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[e] *= old;
-            const int n = min(32, mg.c1 - k0 + 1);
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                if (fi == 0.f) continue;
-                const float4 *o = reinterpret_cast<const float4 *>(a.part_o + slot(k0 + i) * LCA_DC) + lane;
+        for (int e = 0; e < 16; ++e) acc[e] *= old;
+        const int n = min(32, mg.c1 - k0 + 1);
+        for (int i0 = 0; i0 < n; i0 += 4) {
+            float fi[4];
+            float4 x[4][4];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {   // columns 128 v + 4 lane ..
-                    const float4 x = o[32 * v];
-                    acc[4 * v] = fmaf(fi, x.x, acc[4 * v]);
-                    acc[4 * v + 1] = fmaf(fi, x.y, acc[4 * v + 1]);
-                    acc[4 * v + 2] = fmaf(fi, x.z, acc[4 * v + 2]);
-                    acc[4 * v + 3] = fmaf(fi, x.w, acc[4 * v + 3]);
+            for (int i = 0; i < 4; ++i) {
+                fi[i] = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
+                if (i0 + i >= n) fi[i] = 0.f;
+                const float4 *o = reinterpret_cast<const float4 *>(a.part_o + slot(k0 + i0 + i) * LCA_DC) + lane;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)   // columns 128 v + 4 lane ..
+                    x[i][v] = fi[i] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : o[32 * v];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    acc[4 * v] = fmaf(fi[i], x[i][v].x, acc[4 * v]);
+                    acc[4 * v + 1] = fmaf(fi[i], x[i][v].y, acc[4 * v + 1]);
+                    acc[4 * v + 2] = fmaf(fi[i], x[i][v].z, acc[4 * v + 2]);
+                    acc[4 * v + 3] = fmaf(fi[i], x[i][v].w, acc[4 * v + 3]);
                 }
-            }
         }
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        uint16_t *hl = a.o_hl + (size_t(mg.t0 + r / LCA_HEADS) * LCA_HEADS + r % LCA_HEADS) * (2 * LCA_DC) + 4 * lane;
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    uint16_t *hl = a.o_hl + (size_t(mg.t0 + r / LCA_HEADS) * LCA_HEADS + r % LCA_HEADS) * (2 * LCA_DC) + 4 * lane;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            uint32_t hi[2], lo[2];
+    for (int v = 0; v < 4; ++v) {
+        uint32_t hi[2], lo[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float o0 = acc[4 * v + 2 * e] * inv, o1 = acc[4 * v + 2 * e + 1] * inv;
-                hi[e] = pack_bf16(o0, o1);
-                lo[e] = pack_bf16(o0 - bf_lo(hi[e]), o1 - bf_hi(hi[e]));
-            }
-            *reinterpret_cast<uint2 *>(hl + 128 * v) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2 *>(hl + LCA_DC + 128 * v) = make_uint2(lo[0], lo[1]);
+        for (int e = 0; e < 2; ++e) {
+            const float o0 = acc[4 * v + 2 * e] * inv, o1 = acc[4 * v + 2 * e + 1] * inv;
+            hi[e] = pack_bf16(o0, o1);
+            lo[e] = pack_bf16(o0 - bf_lo(hi[e]), o1 - bf_hi(hi[e]));
         }
+        *reinterpret_cast<uint2 *>(hl + 128 * v) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2 *>(hl + LCA_DC + 128 * v) = make_uint2(lo[0], lo[1]);
     }
 }
 
