@@ -455,14 +455,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
-// 32-byte store of eight 32-bit values.
-__device__ __forceinline__ void st_global_32b(void *p, const uint32_t (&v)[8])
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 // A cluster's pieces: query tile q and the cache tiles [k0, k1) of it.
 struct ChunkPiece {
     ChunkTile t;
@@ -817,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
         const uint32_t lane_base = uint32_t(32 * warp) << 16;
         const int pair_bar = 1 + (warp & 1);   // warps w and w + 2 share their rows
         float *xm = reinterpret_cast<float *>(smem + PC_OFF_X);
-        const int tok = 4 * int(cta) + (row >> 4), head = row & 15;
+        const int tok = 4 * int(cta) + (row >> 4);
         const uint32_t peer_sread = map_to_cta(sread(0), 0), peer_pfull = map_to_cta(pfull(0), 0);
         const uint32_t peer_oread = map_to_cta(oread, 0);
         const int sub_shift = min(a.page_shift, 7), subs = PC_TILE >> sub_shift;
@@ -861,6 +853,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 if (lane == 0 && ok) mbar_arrive_pair(peer_sread + 8 * (n & 1));
 
                 const bool edge = row0 + PC_TILE > nv_all;   // the same for both CTAs
+                bool v_due = false;
                 if (edge) {
                     // A row that is not attended by every token enters their
                     // PV product with weight 0, which a NaN or infinity in
@@ -870,7 +863,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     // (a token that does attend the row has the NaN in its
                     // weight already).
                     const int nvs = i + 1 == tiles ? nvs_last : PC_VS;
-                    ok = ok && warp_wait(vready, edges & 1, abort_flag, 16);
+                    bool waited = false;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t odd = 0;
@@ -878,6 +871,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                         for (int x = 0; x < 32; ++x)
                             if (!(fabsf(s[32 * h + x]) <= 3.4e38f)) odd |= 1u << x;
                         odd = __reduce_or_sync(0xffffffffu, odd);
+                        if (odd && !waited) {
+                            ok = ok && warp_wait(vready, edges & 1, abort_flag, 16);
+                            waited = true;
+                        }
                         while (odd && ok) {
                             const int r = 64 * half + 32 * h + __ffs(int(odd)) - 1;
                             odd &= odd - 1;
@@ -892,7 +889,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                             if (__any_sync(0xffffffffu, bad)) *p = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
-                    ++edges;
+                    v_due = !waited;
                 }
                 if (edge || !live || pages != all_pages) {
                     const int32_t left = nv - row0 - 64 * half;
@@ -947,6 +944,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     *reinterpret_cast<uint4 *>(prow + ((e ^ (row & 7)) << 4)) =
                         make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
                 fence_proxy_async();
+                // every edge tile's arrival is taken, so that the next one's can be told apart
+                if (v_due) ok = ok && warp_wait(vready, edges & 1, abort_flag, 16);
+                if (edge) ++edges;
                 if (__any_sync(0xffffffffu, f != 1.f)) {
                     tc_fence_after();
 #pragma unroll 1
@@ -972,43 +972,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 ok = ok && warp_wait(vdone(n - 1), ((n - 1) >> 1) & 1, abort_flag, 23);
                 tc_fence_after();
             }
+            // Rows leave through this warp's quarter of the P buffer (free: PV is
+            // done), 128 bytes of each at a time, so that a store instruction
+            // writes four whole lines: straight from the registers, 32 bytes of 32
+            // rows at once, they took 10000 cycles for a query tile.
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            uint16_t *hl = a.o_hl + (size_t(live ? t : 0) * LCA_HEADS + head) * (2 * LCA_DC) + 256 * half;
-            float *po = a.part_o + (size_t(w.slot < 0 ? 0 : w.slot) * PC_ROWS + 64 * cta + row) * LCA_DC + 256 * half;
             if (w.slot >= 0 && half == 0)
                 *reinterpret_cast<float2 *>(a.part_ml + (size_t(w.slot) * PC_ROWS + 64 * cta + row) * 2) =
                     make_float2(m, l);
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-                float o[32];
-                if (tiles) {
-                    tmem_ld32(tmem + lane_base + PC_TM_O + 32 * c, o);
-                } else {
+            uint8_t *stage = smem + PC_OFF_P + warp * 4096;
+            const int unit = lane & 7, row_w = row & 32;   // of a line; the warp's first row
+            // this warp's rows: line of `dst(row)` each, from staged words
+            const auto store_lines = [&](const uint32_t (&v)[32], auto dst) {
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                        make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = 4 * e + (lane >> 3);   // the warp's i-th row
+                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + i * 128 + ((unit ^ (i & 7)) << 4));
+                    if (4 * int(cta) + ((row_w + i) >> 4) < w.t.live)
+                        *(reinterpret_cast<uint4 *>(dst(row_w + i)) + unit) = x;
                 }
-                if (!live) continue;
+            };
+            const int chunks = w.slot >= 0 ? 8 : 4;   // 32 columns of fp32, or 64 of hi and of lo
+            const bool any_live = 4 * int(cta) + (row_w >> 4) < w.t.live;
+#pragma unroll 1
+            for (int c = 0; c < chunks && any_live; ++c) {
+                float o[32];
+                uint32_t x[32];
+                const auto load = [&](int col) {
+                    if (tiles) {
+                        tmem_ld32(tmem + lane_base + PC_TM_O + col, o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+                };
                 if (w.slot >= 0) {
+                    load(32 * c);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t x[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(o[8 * v + e]);
-                        st_global_32b(po + 32 * c + 8 * v, x);
-                    }
+                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e]);
+                    store_lines(x, [&](int r) {
+                        return a.part_o + (size_t(w.slot) * PC_ROWS + 64 * cta + r) * LCA_DC + 256 * half + 32 * c;
+                    });
                 } else {
+                    uint32_t lo[32];
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        uint32_t hi[8], lo[8];
+                    for (int h = 0; h < 2; ++h) {
+                        load(64 * c + 32 * h);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float o0 = o[16 * v + 2 * e] * inv, o1 = o[16 * v + 2 * e + 1] * inv;
-                            hi[e] = pack_bf16(o0, o1);
-                            lo[e] = pack_bf16(o0 - bf_lo(hi[e]), o1 - bf_hi(hi[e]));
+                        for (int e = 0; e < 16; ++e) {
+                            const float o0 = o[2 * e] * inv, o1 = o[2 * e + 1] * inv;
+                            x[16 * h + e] = pack_bf16(o0, o1);
+                            lo[16 * h + e] = pack_bf16(o0 - bf_lo(x[16 * h + e]), o1 - bf_hi(x[16 * h + e]));
                         }
-                        st_global_32b(hl + 32 * c + 16 * v, hi);
-                        st_global_32b(hl + LCA_DC + 32 * c + 16 * v, lo);
                     }
+                    const auto dst = [&](int r) {
+                        return a.o_hl + (size_t(w.t.t0 + 4 * int(cta) + (r >> 4)) * LCA_HEADS + (r & 15)) * (2 * LCA_DC) +
+                               256 * half + 64 * c;
+                    };
+                    store_lines(x, dst);
+                    store_lines(lo, [&](int r) { return dst(r) + LCA_DC; });
                 }
             }
             if (tiles) {
