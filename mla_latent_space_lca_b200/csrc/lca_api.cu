@@ -529,7 +529,7 @@ ChunkWs chunk_ws_layout(void *ws, int B, int64_t T)
     for (int32_t **f : {&w.plan.q0, &w.plan.q1, &w.plan.tile0}) *f = reinterpret_cast<int32_t *>(take(size_t(B) * 4));
     w.plan.tile = reinterpret_cast<ChunkTile *>(take((size_t(T) / PC_TOKENS + size_t(B) + 1) * sizeof(ChunkTile)));
     w.plan.first = reinterpret_cast<int32_t *>(take(PC_MAX_CLUSTERS * 4));
-    w.plan.nq = reinterpret_cast<int32_t *>(take(4));
+    w.plan.nq = reinterpret_cast<int32_t *>(take(8));
     w.plan.merge = reinterpret_cast<ChunkMerge *>(take(PC_MAX_CLUSTERS * sizeof(ChunkMerge)));
     w.part_o = reinterpret_cast<float *>(take(size_t(2 * PC_MAX_CLUSTERS) * PC_ROWS * LCA_DC * 4));
     w.part_ml = reinterpret_cast<float *>(take(size_t(2 * PC_MAX_CLUSTERS) * PC_ROWS * 2 * 4));
@@ -619,6 +619,8 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
     a.part_o = w.part_o;
     a.part_ml = w.part_ml;
     const int clusters = std::min(std::max(1, dev->sms / 2), PC_MAX_CLUSTERS);
+    const int64_t most = std::max<int64_t>(c.B, c.T / PC_TOKENS + c.B);   // sequences and query tiles
+    const int plan_threads = most <= 128 ? 128 : most <= 256 ? 256 : 1024;
     CUtensorMap map_q, map_k, map_v, map_a, map_w;
     const uint64_t rows = uint64_t(c.n_pages) << c.shift, q_rows = uint64_t(c.T) * LCA_HEADS;
     if ((rc = make_map_rows(&map_q, c.q, q_rows, 1, q_rows, 64)) ||
@@ -630,7 +632,7 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
         return rc;
     {
         Launch l(c.st, K_PAGED_PLAN);
-        const cudaError_t e = launch_ex(paged_chunk_plan_kernel, dim3(1), dim3(1024), 0, c.st, true, a, clusters);
+        const cudaError_t e = launch_ex(paged_chunk_plan_kernel, dim3(1), dim3(plan_threads), 0, c.st, true, a, clusters);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     {
@@ -642,7 +644,7 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
     if (clusters > 1) {
         Launch l(c.st, K_MERGE);
         const cudaError_t e = launch_ex(paged_merge_kernel, dim3(PC_ROWS * 32 / MG_THREADS, clusters - 1),
-                                        dim3(MG_THREADS), 0, c.st, true, a, clusters);
+                                        dim3(MG_THREADS), 0, c.st, true, a);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     Launch l(c.st, K_GEMM);

@@ -53,8 +53,10 @@ constexpr int PC_KWARPS = 3, PC_VWARPS = 2;      // fetch: warps 4 .. 6 for S, 7
 constexpr int PC_WARP_S = 9, PC_WARP_PV = 10;    // MMA issue (CTA 0)
 constexpr int PC_THREADS = 32 * 11;
 constexpr int PC_MAX_CLUSTERS = 80;              // partial outputs: two per cluster
-constexpr int PC_PLAN_BATCH = 1024;              // sequences that the plan keeps in shared memory
-constexpr int PC_OVER = 2;                       // cost of a piece beyond its tiles, in tiles
+constexpr int PC_MIN_UNITS = 3;                  // fewer clusters rather than shorter ranges: every piece is
+                                                 // one more to merge
+constexpr int PC_PLAN_KEPT = 1024;               // sequences, and query tiles, that the plan keeps in shared memory
+constexpr int PC_OVER = 3;                       // cost of a piece beyond its tiles, in tiles
 
 // A query tile: tokens t0 .. t0 + live - 1 of sequence b; token t attends
 // row_base + t rows (within the table).  The work of all query tiles is laid
@@ -71,11 +73,11 @@ struct alignas(16) ChunkMerge {
 };
 
 struct ChunkPlan {
-    int32_t *q0, *q1;        // [B] rows of the batch, clamped and disjoint (batches above PC_PLAN_BATCH)
-    int32_t *tile0;          // [B] first query tile
+    int32_t *q0, *q1;        // [B] rows of the batch, clamped and disjoint (batches above PC_PLAN_KEPT)
+    int32_t *tile0;          // [B] first query tile (likewise)
     ChunkTile *tile;         // [T / 8 + B + 1]; tile[nq].unit0: all units
     int32_t *first;          // [PC_MAX_CLUSTERS] query tile of the cluster's first unit
-    int32_t *nq;             // [1] query tiles
+    int32_t *nq;             // [2] query tiles, clusters with work
     ChunkMerge *merge;       // [PC_MAX_CLUSTERS] by the first border inside; c1 < 0: none
 };
 
@@ -97,7 +99,7 @@ __device__ __forceinline__ int32_t clamp_rows(int64_t n, int64_t max_rows)
 }
 
 // ------------------------------------------------------------ plan
-// Exclusive sum over the block of 1024 threads plus the carry (see block_scan).
+// Exclusive sum over the block plus the carry (see block_scan).
 struct BlockScan64 {
     int64_t wsum[32];
     int64_t carry;
@@ -105,7 +107,7 @@ struct BlockScan64 {
 
 __device__ __forceinline__ int64_t block_scan64(int64_t x, BlockScan64 &sh)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = int(blockDim.x >> 5);
     int64_t v = x;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -115,7 +117,7 @@ __device__ __forceinline__ int64_t block_scan64(int64_t x, BlockScan64 &sh)
     if (lane == 31) sh.wsum[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        int64_t w = sh.wsum[lane];
+        int64_t w = lane < warps ? sh.wsum[lane] : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, w, off);
@@ -125,7 +127,7 @@ __device__ __forceinline__ int64_t block_scan64(int64_t x, BlockScan64 &sh)
     }
     __syncthreads();
     const int64_t excl = v - x + (warp ? sh.wsum[warp - 1] : 0) + sh.carry;
-    const int64_t all = sh.wsum[31];
+    const int64_t all = sh.wsum[warps - 1];
     __syncthreads();
     if (threadIdx.x == 0) sh.carry += all;
     __syncthreads();
@@ -135,12 +137,13 @@ __device__ __forceinline__ int64_t block_scan64(int64_t x, BlockScan64 &sh)
 // One CTA.  Offsets are read as they come: a sequence's rows are
 // [q_start[b], q_start[b+1]) without those of the sequences before it
 // (running maximum) and outside the batch, so the query tiles number at most
-// T / 8 + B.
+// T / 8 + B.  128 to 1024 threads.
 __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs a, int clusters)
 {
     __shared__ BlockScan sc;
     __shared__ BlockScan64 sc64;
-    __shared__ int32_t wmax[32], run_max, sq0[PC_PLAN_BATCH], sq1[PC_PLAN_BATCH], st0[PC_PLAN_BATCH];
+    __shared__ int32_t wmax[32], run_max, sq0[PC_PLAN_KEPT], sq1[PC_PLAN_KEPT], st0[PC_PLAN_KEPT];
+    __shared__ int64_t su0[PC_PLAN_KEPT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         run_max = 0;
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
     griddep_launch_dependents();
     const int64_t max_rows = a.max_blocks << a.page_shift;
     const ChunkPlan &p = a.plan;
-    const bool small = a.B <= PC_PLAN_BATCH;
+    const bool small = a.B <= PC_PLAN_KEPT;
     int32_t *q0s = small ? sq0 : p.q0, *q1s = small ? sq1 : p.q1, *tile0 = small ? st0 : p.tile0;
     for (int base = 0; base < a.B; base += int(blockDim.x)) {
         const int b = base + int(threadIdx.x);
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
         if (lane == 31) wmax[warp] = m;
         __syncthreads();
         if (warp == 0) {
-            int32_t w = wmax[lane];
+            int32_t w = lane < int(blockDim.x >> 5) ? wmax[lane] : 0;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int32_t y = __shfl_up_sync(0xffffffffu, w, off);
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
         m = max(m, run_max);
         if (warp) m = max(m, wmax[warp - 1]);
         __syncthreads();
-        if (threadIdx.x == 0) run_max = max(run_max, wmax[31]);
+        if (threadIdx.x == 0) run_max = max(run_max, wmax[(blockDim.x >> 5) - 1]);
         const int32_t q0 = m, q1 = max(hi, m);
         const int32_t t0 = block_scan(b < a.B ? (q1 - q0 + PC_TOKENS - 1) / PC_TOKENS : 0, 0x3fffffff, sc);
         if (b < a.B) {
@@ -207,37 +210,43 @@ __global__ void __launch_bounds__(1024) paged_chunk_plan_kernel(const ChunkArgs 
             w.tiles = (int64_t(clamp_rows(w.row_base + w.t0 + w.live - 1, max_rows)) + PC_TILE - 1) / PC_TILE;
         }
         w.unit0 = block_scan64(i < nq ? w.tiles + PC_OVER : 0, sc64);
-        if (i < nq) p.tile[i] = w;
+        if (i < nq) {
+            p.tile[i] = w;
+            if (i < PC_PLAN_KEPT) su0[i] = w.unit0;
+        }
     }
     const int64_t units = sc64.carry;
+    const int active = int(min64(clusters, (units + PC_MIN_UNITS - 1) / PC_MIN_UNITS));
     if (threadIdx.x == 0) {
         p.tile[nq].unit0 = units;
-        *p.nq = nq;
+        p.nq[0] = nq;
+        p.nq[1] = active;
     }
     __syncthreads();
-    // Cluster c starts at unit c * units / clusters: its query tile, and whether
+    // Cluster c starts at unit c * units / active: its query tile, and whether
     // that border cuts the tile's cache tiles.
     __shared__ int32_t at_tile[PC_MAX_CLUSTERS];
     __shared__ bool cuts[PC_MAX_CLUSTERS];
+    const auto unit0 = [&](int i) { return nq <= PC_PLAN_KEPT ? su0[i] : p.tile[i].unit0; };
     const int c = threadIdx.x;
-    if (c < clusters && nq > 0) {
-        const int64_t at = split_begin(c, units, clusters);
+    if (c < active) {
+        const int64_t at = split_begin(c, units, active);
         int lo = 0, hi = nq - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (p.tile[mid].unit0 <= at) lo = mid;
+            if (unit0(mid) <= at) lo = mid;
             else hi = mid - 1;
         }
         p.first[c] = lo;
         at_tile[c] = lo;
-        cuts[c] = at < units && at > p.tile[lo].unit0 + PC_OVER;
+        cuts[c] = at > unit0(lo) + PC_OVER;
     }
     __syncthreads();
     if (c < clusters) {
         ChunkMerge g{0, 0, 0, -1};
-        if (nq > 0 && c > 0 && cuts[c] && !(cuts[c - 1] && at_tile[c - 1] == at_tile[c])) {
+        if (c > 0 && c < active && cuts[c] && !(cuts[c - 1] && at_tile[c - 1] == at_tile[c])) {
             g = ChunkMerge{p.tile[at_tile[c]].t0, p.tile[at_tile[c]].live, c - 1, c};
-            while (g.c1 + 1 < clusters && cuts[g.c1 + 1] && at_tile[g.c1 + 1] == at_tile[c]) ++g.c1;
+            while (g.c1 + 1 < active && cuts[g.c1 + 1] && at_tile[g.c1 + 1] == at_tile[c]) ++g.c1;
         }
         p.merge[c] = g;
     }
@@ -473,14 +482,19 @@ struct ChunkPiece {
 struct ChunkRange {
     int32_t q, nq, cluster;
     int64_t begin, end;
-    __device__ __forceinline__ ChunkRange(const ChunkPlan &p, int c, int clusters)
+    __device__ __forceinline__ ChunkRange(const ChunkPlan &p, int c)
     {
-        nq = *p.nq;
+        nq = p.nq[0];
+        const int active = p.nq[1];
         cluster = c;
-        const int64_t units = nq ? p.tile[nq].unit0 : 0;
-        begin = split_begin(c, units, clusters);
-        end = split_begin(c + 1, units, clusters);
-        q = begin < end ? p.first[c] : nq;
+        q = nq;
+        begin = end = 0;
+        if (c < active) {
+            const int64_t units = p.tile[nq].unit0;
+            begin = split_begin(c, units, active);
+            end = split_begin(c + 1, units, active);
+            q = p.first[c];
+        }
     }
     // the next piece with cache tiles, or of a query tile that has none
     __device__ __forceinline__ bool next(const ChunkPlan &p, ChunkPiece &w)
@@ -557,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     griddep_wait();   // the plan, and everything earlier in the stream
 
     const int64_t max_rows = a.max_blocks << a.page_shift;
-    ChunkRange range(a.plan, int(blockIdx.x >> 1), int(gridDim.x >> 1));
+    ChunkRange range(a.plan, int(blockIdx.x >> 1));
     ChunkPiece w;
 
     // ---------------------------------------------------------------- producers
@@ -981,27 +995,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 *reinterpret_cast<float2 *>(a.part_ml + (size_t(w.slot) * PC_ROWS + 64 * cta + row) * 2) =
                     make_float2(m, l);
             uint8_t *stage = smem + PC_OFF_P + warp * 4096;
-            const int unit = lane & 7, row_w = row & 32;   // of a line; the warp's first row
-            // this warp's rows: line of `dst(row)` each, from staged words
-            const auto store_lines = [&](const uint32_t (&v)[32], auto dst) {
+            const int row_w = row & 32;                                          // the warp's first row
+            const int rows_live = LCA_HEADS * (w.t.live - 4 * int(cta)) - row_w;   // of the warp's 32
+            // 128 bytes of each of the warp's rows, `pitch` bytes apart from `dst` on
+            const auto store_lines = [&](const uint32_t (&v)[32], void *dst, int pitch) {
                 __syncwarp();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
                         make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 __syncwarp();
+                uint4 x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int i = 4 * e + (lane >> 3);   // the warp's i-th row
-                    const uint4 x = *reinterpret_cast<const uint4 *>(stage + i * 128 + ((unit ^ (i & 7)) << 4));
-                    if (4 * int(cta) + ((row_w + i) >> 4) < w.t.live)
-                        *(reinterpret_cast<uint4 *>(dst(row_w + i)) + unit) = x;
+                    const int i = 4 * e + (lane >> 3);
+                    x[e] = *reinterpret_cast<const uint4 *>(stage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
                 }
+                uint8_t *line = static_cast<uint8_t *>(dst) + (lane >> 3) * pitch + (lane & 7) * 16;
+#pragma unroll
+                for (int e = 0; e < 8; ++e, line += 4 * pitch)
+                    if (4 * e + (lane >> 3) < rows_live) *reinterpret_cast<uint4 *>(line) = x[e];
             };
             const int chunks = w.slot >= 0 ? 8 : 4;   // 32 columns of fp32, or 64 of hi and of lo
-            const bool any_live = 4 * int(cta) + (row_w >> 4) < w.t.live;
 #pragma unroll 1
-            for (int c = 0; c < chunks && any_live; ++c) {
+            for (int c = 0; c < chunks && rows_live > 0; ++c) {
                 float o[32];
                 uint32_t x[32];
                 const auto load = [&](int col) {
@@ -1016,9 +1033,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     load(32 * c);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e]);
-                    store_lines(x, [&](int r) {
-                        return a.part_o + (size_t(w.slot) * PC_ROWS + 64 * cta + r) * LCA_DC + 256 * half + 32 * c;
-                    });
+                    store_lines(x, a.part_o + (size_t(w.slot) * PC_ROWS + 64 * cta + row_w) * LCA_DC + 256 * half + 32 * c,
+                                LCA_DC * 4);
                 } else {
                     uint32_t lo[32];
 #pragma unroll
@@ -1031,12 +1047,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                             lo[16 * h + e] = pack_bf16(o0 - bf_lo(x[16 * h + e]), o1 - bf_hi(x[16 * h + e]));
                         }
                     }
-                    const auto dst = [&](int r) {
-                        return a.o_hl + (size_t(w.t.t0 + 4 * int(cta) + (r >> 4)) * LCA_HEADS + (r & 15)) * (2 * LCA_DC) +
-                               256 * half + 64 * c;
-                    };
-                    store_lines(x, dst);
-                    store_lines(lo, [&](int r) { return dst(r) + LCA_DC; });
+                    // (rows of a query tile follow one another, token by token, head by head)
+                    uint16_t *dst = a.o_hl + (size_t(w.t.t0 + 4 * int(cta)) * LCA_HEADS + row_w) * (2 * LCA_DC) +
+                                    256 * half + 64 * c;
+                    store_lines(x, dst, 4 * LCA_DC);
+                    store_lines(lo, dst + LCA_DC, 4 * LCA_DC);
                 }
             }
             if (tiles) {
@@ -1060,10 +1075,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
 // sum_s 2^(m_s - M) l_s per query row, one warp each (lane: 16 columns),
 // written as hi + lo.  blockIdx.y + 1 is the first border inside the query
 // tile, which starts in cluster c0 = blockIdx.y and has pieces of all clusters
-// to c1 (a range between equal borders holds none).
+// to c1.
 constexpr int MG_THREADS = 256;
 
-__global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs a, int clusters)
+__global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs a)
 {
     griddep_wait();
     griddep_launch_dependents();
@@ -1072,7 +1087,6 @@ __global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs
     const int r = int(blockIdx.x) * (MG_THREADS / 32) + int(threadIdx.x >> 5);   // query row
     const ChunkMerge mg = p.merge[blockIdx.y + 1];
     if (mg.c1 < 0 || r / LCA_HEADS >= mg.live) return;
-    const int64_t units = p.tile[*p.nq].unit0;
     const auto slot = [&](int k) { return size_t(k == mg.c0 ? 2 * k + 1 : 2 * k) * PC_ROWS + r; };
     float M = -1e30f, den = 0.f, acc[16];
 #pragma unroll
@@ -1081,9 +1095,7 @@ __global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs
     for (int k0 = mg.c0; k0 <= mg.c1; k0 += 32) {
         const int k = k0 + lane;
         float2 ml = make_float2(-1e30f, 0.f);
-        // (fewer units than clusters: ranges without any)
-        if (k <= mg.c1 && (units >= clusters || split_begin(k, units, clusters) < split_begin(k + 1, units, clusters)))
-            ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(k) * 2);
+        if (k <= mg.c1) ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(k) * 2);
         float top = ml.x;
 #pragma unroll
         for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
