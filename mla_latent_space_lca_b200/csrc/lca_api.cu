@@ -1217,8 +1217,9 @@ int mla_paged_attn(const void *pages, int64_t n_pages, int page_size, const int3
     if (B < 1 || T < 0 || n_pages < 1 || page_size < 1 || max_blocks < 1 || max_new < 1) return LCA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || scale <= 0.f) return LCA_ERR_INVALID_ARG;
     const int shift = page_shift(page_size);
-    if (shift < 0 || n_pages > (int64_t(0x7fffffff) >> shift) || max_blocks > (int64_t(0x7fffffff) >> shift) ||
-        T >= (int64_t(1) << 27))
+    // row indexes are int32, and may run on to the end of a cache tile and the next one's first pages
+    constexpr int64_t most_rows = (int64_t(1) << 31) - 1024;
+    if (shift < 0 || n_pages > (most_rows >> shift) || max_blocks > (most_rows >> shift) || T >= (int64_t(1) << 27))
         return LCA_ERR_UNSUPPORTED;
     // single tokens: tile offsets are int32, so all tokens' tiles together must stay below 2^30
     if (max_new == 1 && T * (((max_blocks << shift) + AT_TILE - 1) / AT_TILE) >= (int64_t(1) << 30))
