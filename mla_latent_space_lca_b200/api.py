@@ -375,7 +375,7 @@ def _on(dev, stream, fn, *args):
     """fn(*args, stream) with dev as the current device, on `stream` or dev's
     current stream.  (A server makes a handful of these calls per token: the
     device guard is entered only where another device is current.)"""
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _on(dev, stream, fn, *args)
     return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
@@ -437,11 +437,7 @@ def lca_page_tables(ctx_lens, new_lens, free_pages, taken, block_table, page_siz
     return seq_lens, q_start, slot_map, positions, taken_out, counts
 
 
-def lca_append_paged(pages, rows, slot_map, stream=None):
-    """rows [T, 576] (bf16, rows may lie apart: a slice of a wider tensor)
-    into pages [n_pages, page_size, 576] at slots slot_map [T] (int64,
-    page * page_size + row); slots outside the pages, such as -1, are
-    skipped.  Slots must be distinct."""
+def _append_args(pages, rows, slot_map):
     _pages(pages)
     if not isinstance(rows, torch.Tensor) or not rows.is_cuda or rows.dtype != torch.bfloat16:
         raise TypeError("rows must be a CUDA bfloat16 tensor")
@@ -454,8 +450,25 @@ def lca_append_paged(pages, rows, slot_map, stream=None):
     if step != 1 or pitch < D:
         raise ValueError(f"rows must not overlap and hold contiguous vectors (strides {rows.stride()})")
     _need(slot_map, "slot_map", torch.int64, (T,))
-    rc = _on(_same_device(pages, "rows slot_map", rows, slot_map), stream, _lib.lib().lca_append_paged,
-             rows.data_ptr(), pitch, slot_map.data_ptr(), T, pages.data_ptr(), *pages.shape[:2])
+    return (_same_device(pages, "rows slot_map", rows, slot_map), *pages.shape[:2], T, pitch)
+
+
+def lca_append_paged(pages, rows, slot_map, stream=None):
+    """rows [T, 576] (bf16, rows may lie apart: a slice of a wider tensor)
+    into pages [n_pages, page_size, 576] at slots slot_map [T] (int64,
+    page * page_size + row); slots outside the pages, such as -1, are
+    skipped.  Slots must be distinct."""
+    try:   # the usual call at once: its checks cost as much as the launch otherwise
+        dev, (n_pages, page, width), (T, vec), (pitch, step) = pages.get_device(), pages.shape, rows.shape, rows.stride()
+        usual = (dev >= 0 and width == vec == D and step == 1 and pitch >= D and pages.dtype is rows.dtype is torch.bfloat16
+                 and rows.get_device() == dev and slot_map.get_device() == dev and slot_map.dtype is torch.int64
+                 and slot_map.shape == (T,) and pages.is_contiguous() and slot_map.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        dev, n_pages, page, T, pitch = _append_args(pages, rows, slot_map)
+    rc = _on(dev, stream, _lib.lib().lca_append_paged, rows.data_ptr(), pitch, slot_map.data_ptr(), T, pages.data_ptr(),
+             n_pages, page)
     if rc:
         check(rc, "lca_append_paged")
 
