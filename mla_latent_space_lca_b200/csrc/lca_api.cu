@@ -507,6 +507,10 @@ PagedWs paged_ws_layout(void *ws, int64_t T)
     return w;
 }
 
+// Threads of a one-CTA kernel over n things: a barrier of 128 threads takes a
+// few tens of cycles, one of 1024 a few hundred.
+unsigned block_for(int64_t n) { return n <= 128 ? 128 : n <= 256 ? 256 : 1024; }
+
 // Workspace of the chunk kernel: the plan, the pieces' partial outputs and o
 // as hi + lo for the W_UV product.
 struct ChunkWs {
@@ -557,7 +561,7 @@ int run_paged_tokens(DeviceInfo *dev, const PagedCall &c, const PagedWs &w)
     const int T = int(c.T);
     {
         Launch l(c.st, K_PAGED_PLAN);
-        const cudaError_t e = launch_ex(paged_plan_kernel, dim3(1), dim3(1024), 0, c.st, true, c.seq_lens, c.q_start,
+        const cudaError_t e = launch_ex(paged_plan_kernel, dim3(1), dim3(block_for(std::max(T, c.B))), 0, c.st, true, c.seq_lens, c.q_start,
                                         c.B, T, max_rows, w.item_seq, w.item_len, w.tile_start);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
@@ -620,7 +624,6 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
     a.part_ml = w.part_ml;
     const int clusters = std::min(std::max(1, dev->sms / 2), PC_MAX_CLUSTERS);
     const int64_t most = std::max<int64_t>(c.B, c.T / PC_TOKENS + c.B);   // sequences and query tiles
-    const int plan_threads = most <= 128 ? 128 : most <= 256 ? 256 : 1024;
     CUtensorMap map_q, map_k, map_v, map_a, map_w;
     const uint64_t rows = uint64_t(c.n_pages) << c.shift, q_rows = uint64_t(c.T) * LCA_HEADS;
     if ((rc = make_map_rows(&map_q, c.q, q_rows, 1, q_rows, 64)) ||
@@ -632,7 +635,7 @@ int run_paged_chunks(DeviceInfo *dev, const PagedCall &c, const ChunkWs &w)
         return rc;
     {
         Launch l(c.st, K_PAGED_PLAN);
-        const cudaError_t e = launch_ex(paged_chunk_plan_kernel, dim3(1), dim3(plan_threads), 0, c.st, true, a, clusters);
+        const cudaError_t e = launch_ex(paged_chunk_plan_kernel, dim3(1), dim3(block_for(most)), 0, c.st, true, a, clusters);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     {
@@ -1162,7 +1165,7 @@ int lca_page_tables(const int32_t *ctx_lens, const int32_t *new_lens, const int3
     cudaLaunchConfig_t cfg{};
     const unsigned ctas = max_tokens > 2048 ? 8 : 1;
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(1024);
+    cfg.blockDim = dim3(ctas > 1 ? 1024 : block_for(std::max<int64_t>(B, max_tokens / 2)));
     cfg.dynamicSmemBytes = tables_smem(B);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];

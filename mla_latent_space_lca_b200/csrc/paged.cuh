@@ -11,7 +11,7 @@ namespace lca {
 constexpr int K_TABLES = 10, K_APPEND_PAGED = 11, K_PAGED_PLAN = 12;
 
 // ------------------------------------------------------------ scans
-// Inclusive scan of one int per thread over a block of 1024, with a running
+// Inclusive scan of one int per thread over a block, with a running
 // carry for the chunks before; sums saturate at `cap` (a + b with a, b <= cap
 // < 2^30 does not overflow, and min(cap, .) of sums of non-negative terms is
 // associative).  Returns the exclusive sum; *total becomes the sum so far.
@@ -66,7 +66,7 @@ __device__ __forceinline__ int last_le(const int32_t *v, int n, int32_t x)
 }
 
 // ------------------------------------------------------------ page tables
-// One cluster of CTAs.  Every CTA scans the batch (two scans: tokens, then
+// One cluster of CTAs of 128 to 1024 threads.  Every CTA scans the batch (two scans: tokens, then
 // the pages they need) into shared memory; then the CTAs share the tokens and
 // the new table entries out among themselves.  An entry that already stands
 // in the table is only read, a new one only written (its page comes from the
@@ -213,7 +213,10 @@ __global__ void __launch_bounds__(APG_THREADS) append_paged_kernel(const uint16_
 // it attends (its position + 1; 0 where it has none, -1 for a row of the
 // batch that belongs to no sequence) and its first tile in the batch's tile
 // list.  q_start is read as it comes: a token t belongs to the sequence b
-// that the search finds, if q_start[b] <= t < q_start[b + 1].  One CTA.
+// that the search finds, if q_start[b] <= t < q_start[b + 1].  One CTA of 128
+// to 1024 threads.
+constexpr int PL_KEPT = 1024;
+
 __global__ void __launch_bounds__(1024) paged_plan_kernel(const int32_t *__restrict__ seq_lens,
                                                           const int32_t *__restrict__ q_start, int B, int T,
                                                           int64_t max_rows, int32_t *__restrict__ item_seq,
@@ -221,17 +224,22 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const int32_t *__restr
                                                           int32_t *__restrict__ tile_start)
 {
     __shared__ BlockScan sh;
+    __shared__ int32_t starts[PL_KEPT + 1];   // q_start, for the search: a step in memory takes ~700 cycles
     if (threadIdx.x == 0) sh.carry = 0;
-    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
+    const bool kept = B <= PL_KEPT;
+    if (kept)
+        for (int b = threadIdx.x; b <= B; b += int(blockDim.x)) starts[b] = q_start[b];
+    const int32_t *qs = kept ? starts : q_start;
+    __syncthreads();
     const int32_t kAll = 0x3fffffff;   // the host keeps the tile count below
     for (int base = 0; base < T; base += int(blockDim.x)) {
         const int t = base + int(threadIdx.x);
         int32_t len = -1, b = 0;
         if (t < T) {
-            b = last_le(q_start, B, t);
-            const int32_t q0 = q_start[b], q1 = q_start[b + 1];
+            b = last_le(qs, B, t);
+            const int32_t q0 = qs[b], q1 = qs[b + 1];
             if (q0 <= t && t < q1) {
                 const int64_t n = int64_t(seq_lens[b]) - (int64_t(q1) - t) + 1;   // position + 1
                 len = int32_t(n < 0 ? 0 : min64(n, max_rows));
