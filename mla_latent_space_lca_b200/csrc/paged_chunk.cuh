@@ -18,8 +18,30 @@
 // A tile is fetched in slots of 8 KB: nine for S ([64 rows][64 columns], this
 // CTA's rows) and eight for PV ([16 rows][256 columns], this CTA's columns),
 // each freed by the commit of the MMAs that read it.  S and PV have a ring of
-// slots each: only where one warp uses and frees a ring's slots in order does
-// the parity of a slot's barrier tell two of its uses apart.
+// slots each (one tile's): only where one warp uses and frees a ring's slots in
+// order does the parity of a slot's barrier tell two of its uses apart.
+//
+// Online softmax: per query row a reference m, raised (and O rescaled) only
+// when the maximum grows by more than 2^8; the weights 2^(z - m) enter PV as
+// bf16 (off by 2^-8 at most, the operand's type), their sum l is of the fp32
+// values.  o = O / l leaves as two bf16 values, hi + lo (off by 2^-16), for the
+// W_UV product of paged_wuv.cuh.
+//
+// What bounds it: per cache tile and pair 36 S steps of 34 cycles and 16 PV
+// steps of 66, 2270 cycles of tensor core for 17.8 MFLOP a CTA (96% of the
+// dense peak; M = 256 would leave no tensor memory for S, tiles of 64 rows
+// would double the reads of Q, 2950 cycles).  Measured, 2048 tokens over 32768
+// rows: 3000 cycles a tile, 1.62 ms for the kernel, 1.40 PFLOP/s, tensor pipe
+// active 75%, at the power cap's 1.6 GHz; 1.9 ms a call back to back.  What
+// holds the rest is the chain from a tile's S through softmax, P and PV to the
+// next P (there is room for one P beside the rings): without any product or
+// copy the same loops take 1.1 ms.
+// With few tokens a sequence the rows come from memory: 16 x 2..5 tokens over
+// 138515 rows, 160 MB, 47 us, of which 8 are the first tile's way through.
+//
+// Work: paged_chunk_plan_kernel lays the query tiles' cache tiles end to end
+// and cuts them into one equal range per pair; a query tile that a border cuts
+// leaves partial (O, m, l) per piece, merged in order by paged_merge_kernel.
 #pragma once
 #include <type_traits>
 
@@ -45,7 +67,7 @@ constexpr int PC_OFF_BAR = PC_OFF_X + 2 * 128 * 4;
 constexpr int PC_BARS = 2 * PC_SLOTS + 13;
 constexpr int PC_OFF_MISC = PC_OFF_BAR + 8 * PC_BARS;
 constexpr int PC_SMEM = PC_OFF_MISC + 16;
-constexpr int PC_SMEM_ALLOC = PC_SMEM;   // no room to align it: the kernel checks that it starts at 1024 bytes
+constexpr int PC_SMEM_ALLOC = PC_SMEM + 1024;
 static_assert(PC_SMEM_ALLOC <= 227 * 1024, "one CTA per SM");
 constexpr uint32_t PC_TM_O = 0, PC_TM_S = 256;   // O 256 columns, S two buffers of 64
 constexpr int PC_SOFTMAX = 4;                    // warps 0 .. 3
@@ -56,7 +78,8 @@ constexpr int PC_MAX_CLUSTERS = 80;              // partial outputs: two per clu
 constexpr int PC_MIN_UNITS = 3;                  // fewer clusters rather than shorter ranges: every piece is
                                                  // one more to merge
 constexpr int PC_PLAN_KEPT = 1024;               // sequences, and query tiles, that the plan keeps in shared memory
-constexpr int PC_OVER = 3;                       // cost of a piece beyond its tiles, in tiles
+constexpr int PC_OVER = 3;                       // cost of a piece beyond its tiles, in tiles: a piece of n tiles
+                                                 // takes 5.2 + 1.65 n us
 
 // A query tile: tokens t0 .. t0 + live - 1 of sequence b; token t attends
 // row_base + t rows (within the table).  The work of all query tiles is laid
@@ -519,12 +542,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, const ChunkArgs a)
 {
-    extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ uint8_t pc_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(pc_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    if (sbase & 1023u) {   // the same in every CTA
-        report_timeout(K_CHUNK, 0);
-        return;
-    }
     const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     uint32_t cta;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(cta));
@@ -577,8 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
     // ---------------------------------------------------------------- producers
     // One thread each; producer p of STEP brings a ring's uses p, p + STEP, ...
     // (wait, expect and copy take it ~400 cycles a slot; the MMAs use a slot of
-    // either ring every 250 to 280).  STEP < ring, so a producer has seen the use
-    // before last of its next slot freed.
+    // either ring every 330).  STEP < ring, so a producer has seen the use before
+    // last of its next slot freed.
     const auto produce = [&](auto is_k_, uint32_t p) {
         constexpr bool K = decltype(is_k_)::value;
         constexpr uint32_t RING = K ? PC_KRING : PC_VRING, STEP = K ? PC_KWARPS : PC_VWARPS;
