@@ -49,6 +49,8 @@
 // result is exact either way).  Each CTA writes one (O, m, l) partial per
 // sequence piece it owns; tail_decode_kernel merges them.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace lca {
@@ -80,6 +82,8 @@ constexpr int AT_ALB = 200;                              // floats per softmax w
 constexpr int AT_ALB_SC = 72;                            // offset of the importance halves
 constexpr int AT_SMEM = AT_OFF_ALB + 4 * AT_ALB * 4;     // 226944
 constexpr int AT_SMEM_ALLOC = AT_SMEM + 1024;           // + alignment slack
+constexpr int AT_SMEM_PLAN = 4 * (4 * 128 + 2 + 4);     // a small paged batch's item list, behind AT_SMEM
+static_assert(AT_SMEM_ALLOC + AT_SMEM_PLAN <= 227 * 1024, "one CTA per SM");
 
 enum { MODE_MLA = 0, MODE_REPS = 1, MODE_LCA = 2 };
 
@@ -117,7 +121,15 @@ struct AttnArgs {
     int64_t max_blocks;
     int64_t n_pages;
     int page_shift;
+    // a small batch (AT_PLAN_ITEMS tokens and sequences at most): every CTA
+    // makes the item list itself, and the first one writes what the tail
+    // reads; NULL: a kernel in front has made it
+    const int32_t *q_start;
+    const int32_t *seq_lens;
+    int n_seq;
+    int32_t *tile_start_out, *item_len_out;
 };
+constexpr int AT_PLAN_ITEMS = 128;
 
 // Shared-memory layout of a 64-row tile.  A contiguous cache's tile arrives as
 // nine [64 rows x 64 columns] blocks.  A paged cache's tile arrives page by
@@ -338,11 +350,79 @@ __device__ __forceinline__ void load_q_rows(const uint16_t *qb, const uint16_t *
     }
 }
 
+// The last index i in [0, n) with v[i] <= x (v non-decreasing, v[0] <= x).
+__device__ __forceinline__ int last_le(const int32_t *v, int n, int32_t x)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (v[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Token t of a batch as an item: its sequence b (the one that the search in
+// q_start finds, if q_start[b] <= t < q_start[b + 1]) and the rows it attends
+// (position + 1; 0 where it has none, -1 for a row of no sequence).
+__device__ __forceinline__ int32_t token_rows(const int32_t *q_start, const int32_t *seq_lens, int n_seq, int t,
+                                              int64_t max_rows, int &b)
+{
+    b = last_le(q_start, n_seq, t);
+    const int32_t q0 = q_start[b], q1 = q_start[b + 1];
+    if (t < q0 || t >= q1) return -1;
+    const int64_t n = int64_t(seq_lens[b]) - (int64_t(q1) - t) + 1;
+    return int32_t(n < 0 ? 0 : min64(n, max_rows));
+}
+
+// The item list of a batch of AT_PLAN_ITEMS tokens and sequences at most, made
+// by each CTA in its shared memory (1 us; a kernel of its own in front costs 3
+// to 4).  Every thread of the block calls it.
+__device__ __forceinline__ void plan_small_batch(AttnArgs &a, int32_t *sh)
+{
+    int32_t *tile_start = sh, *len = tile_start + AT_PLAN_ITEMS + 1, *seq = len + AT_PLAN_ITEMS;
+    int32_t *starts = seq + AT_PLAN_ITEMS, *sums = starts + AT_PLAN_ITEMS + 1;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    for (int b = t; b <= a.n_seq; b += int(blockDim.x)) starts[b] = a.q_start[b];
+    __syncthreads();
+    int32_t rows = 0, tiles = 0, upto = 0;
+    int b = 0;
+    if (t < AT_PLAN_ITEMS) {
+        if (t < a.B) rows = token_rows(starts, a.seq_lens, a.n_seq, t, a.L, b);
+        tiles = rows > 0 ? (rows + AT_TILE - 1) / AT_TILE : 0;
+        upto = tiles;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        if (lane == 31) sums[warp] = upto;
+    }
+    __syncthreads();
+    if (t < a.B) {
+        for (int w = 0; w < warp; ++w) upto += sums[w];
+        tile_start[t] = upto - tiles;
+        len[t] = rows;
+        seq[t] = b;
+        if (t == a.B - 1) tile_start[a.B] = upto;
+        if (blockIdx.x == 0) {
+            a.tile_start_out[t] = upto - tiles;
+            a.item_len_out[t] = rows;
+            if (t == a.B - 1) a.tile_start_out[a.B] = upto;
+        }
+    }
+    __syncthreads();
+    a.tile_start = tile_start;
+    a.lens = len;
+    a.item_seq = seq;
+}
+
 template <int MODE, bool VARLEN = false, bool PAGED = false>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_cache,
-                       const __grid_constant__ CUtensorMap map_rep, const AttnArgs a)
+                       const __grid_constant__ CUtensorMap map_rep, const AttnArgs args)
 {
+    std::conditional_t<PAGED, AttnArgs, const AttnArgs &> a = args;
     static_assert(!PAGED || (MODE == MODE_MLA && VARLEN), "pages: plain rows of a ragged batch");
     using Lay = TileLayout<PAGED>;
     extern __shared__ uint8_t at_smem_raw[];
@@ -408,6 +488,9 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     // a ragged batch's tile list comes from the kernel before: wait for it
     // (and so for everything earlier in the stream) before reading it
     if constexpr (VARLEN) griddep_wait();
+    if constexpr (PAGED) {
+        if (a.q_start) plan_small_batch(a, reinterpret_cast<int32_t *>(smem + AT_SMEM));
+    }
     const int64_t T = VARLEN ? int64_t(a.tile_start[a.B]) : a.T;
     const int c = blockIdx.x;
     const int64_t t_begin = split_begin(c, T, a.G);

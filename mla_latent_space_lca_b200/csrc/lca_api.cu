@@ -71,7 +71,7 @@ int current_device(DeviceInfo **out)
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_MLA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_LCA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_REPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
-        good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_MLA, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC) == cudaSuccess;
+        good &= cudaFuncSetAttribute(attn_decode_kernel<MODE_MLA, true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, AT_SMEM_ALLOC + AT_SMEM_PLAN) == cudaSuccess;
         good &= cudaFuncSetAttribute(tail_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TD_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(paged_wuv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PW_SMEM_ALLOC) == cudaSuccess;
         good &= cudaFuncSetAttribute(paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PC_SMEM_ALLOC) == cudaSuccess;
@@ -559,7 +559,8 @@ int run_paged_tokens(DeviceInfo *dev, const PagedCall &c, const PagedWs &w)
     if (rc) return rc;
     const int64_t max_rows = c.max_blocks << c.shift;
     const int T = int(c.T);
-    {
+    const bool small = T <= AT_PLAN_ITEMS && c.B <= AT_PLAN_ITEMS;
+    if (!small) {
         Launch l(c.st, K_PAGED_PLAN);
         const cudaError_t e = launch_ex(paged_plan_kernel, dim3(1), dim3(block_for(std::max(T, c.B))), 0, c.st, true, c.seq_lens, c.q_start,
                                         c.B, T, max_rows, w.item_seq, w.item_len, w.tile_start);
@@ -585,10 +586,17 @@ int run_paged_tokens(DeviceInfo *dev, const PagedCall &c, const PagedWs &w)
     a.max_blocks = c.max_blocks;
     a.n_pages = c.n_pages;
     a.page_shift = c.shift;
+    if (small) {
+        a.q_start = c.q_start;
+        a.seq_lens = c.seq_lens;
+        a.n_seq = c.B;
+        a.tile_start_out = w.tile_start;
+        a.item_len_out = w.item_len;
+    }
     {
         Launch l(c.st, K_ATTN);
         const cudaError_t e = launch_ex(attn_decode_kernel<MODE_MLA, true, true>, dim3(a.G), dim3(AT_THREADS),
-                                        AT_SMEM_ALLOC, c.st, true, map_pages, map_pages, a);
+                                        AT_SMEM_ALLOC + AT_SMEM_PLAN, c.st, true, map_pages, map_pages, a);
         if (e != cudaSuccess || (rc = l.done())) return LCA_ERR_CUDA;
     }
     Launch l(c.st, K_COMBINE);

@@ -53,18 +53,6 @@ __device__ __forceinline__ int32_t block_scan(int32_t x, int32_t cap, BlockScan 
     return excl;
 }
 
-// The last index i in [0, n) with v[i] <= x (v non-decreasing, v[0] <= x).
-__device__ __forceinline__ int last_le(const int32_t *v, int n, int32_t x)
-{
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (v[mid] <= x) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
 // ------------------------------------------------------------ page tables
 // One cluster of CTAs of 128 to 1024 threads.  Every CTA scans the batch (two scans: tokens, then
 // the pages they need) into shared memory; then the CTAs share the tokens and
@@ -209,12 +197,9 @@ __global__ void __launch_bounds__(APG_THREADS) append_paged_kernel(const uint16_
 }
 
 // ------------------------------------------------------------ attention: the work list
-// Every token of the batch as one item: the sequence it belongs to, the rows
-// it attends (its position + 1; 0 where it has none, -1 for a row of the
-// batch that belongs to no sequence) and its first tile in the batch's tile
-// list.  q_start is read as it comes: a token t belongs to the sequence b
-// that the search finds, if q_start[b] <= t < q_start[b + 1].  One CTA of 128
-// to 1024 threads.
+// Every token of the batch as one item (token_rows) and its first tile in the
+// batch's tile list, for batches that the attention kernel does not list
+// itself.  One CTA of 128 to 1024 threads.
 constexpr int PL_KEPT = 1024;
 
 __global__ void __launch_bounds__(1024) paged_plan_kernel(const int32_t *__restrict__ seq_lens,
@@ -236,15 +221,9 @@ __global__ void __launch_bounds__(1024) paged_plan_kernel(const int32_t *__restr
     const int32_t kAll = 0x3fffffff;   // the host keeps the tile count below
     for (int base = 0; base < T; base += int(blockDim.x)) {
         const int t = base + int(threadIdx.x);
-        int32_t len = -1, b = 0;
-        if (t < T) {
-            b = last_le(qs, B, t);
-            const int32_t q0 = qs[b], q1 = qs[b + 1];
-            if (q0 <= t && t < q1) {
-                const int64_t n = int64_t(seq_lens[b]) - (int64_t(q1) - t) + 1;   // position + 1
-                len = int32_t(n < 0 ? 0 : min64(n, max_rows));
-            }
-        }
+        int32_t len = -1;
+        int b = 0;
+        if (t < T) len = token_rows(qs, seq_lens, B, t, max_rows, b);
         const int32_t tiles = len > 0 ? (len + AT_TILE - 1) / AT_TILE : 0;
         const int32_t t0 = block_scan(tiles, kAll, sh);
         if (t < T) {

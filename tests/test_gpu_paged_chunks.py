@@ -180,3 +180,17 @@ def test_refusals_on_the_gpu():
         lca.mla_paged_attn(pages, table, lens, start, q, w_uv, 0)
     empty = lca.mla_paged_attn(pages, table, lens, i32([0, 0]), q[:0], w_uv, 4)
     assert empty.shape == (0, 16, 128)
+
+
+@pytest.mark.parametrize("B", [127, 128, 129, 300, 1030])
+def test_single_tokens_of_many_sequences(B):
+    # up to 128 tokens and sequences the attention kernel lists its items itself
+    rng = random.Random(B)
+    new = [rng.choice([0, 1, 1, 1]) for _ in range(B)]
+    lens = [n + rng.randrange(200) for n in new]
+    check_attn(*make(lens, new, 16, seed=B, pad=2), 1)
+
+
+@pytest.mark.parametrize("new", [[128], [1] * 128, [129], [0] * 127 + [5], [60, 0, 68]])
+def test_item_lists_at_their_size(new):
+    check_attn(*make([n + 50 for n in new], new, 32, seed=len(new)), 1)
