@@ -293,9 +293,7 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar)
 }
 
 // One lane of the (converged) warp, the same each time.  MMAs issued under it
-// take 26 to 37 cycles each as long as little else is under it (80 under `lane
-// == 0`, and where whole loops run in one lane): the loops and the waits stay
-// with the whole warp.
+// take 26 to 37 cycles each (80 under `lane == 0`).
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t p;
@@ -303,6 +301,7 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+// mbar_try_wait without its wait.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
