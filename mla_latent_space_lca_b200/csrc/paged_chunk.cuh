@@ -78,8 +78,9 @@ constexpr int PC_MAX_CLUSTERS = 80;              // partial outputs: two per clu
 constexpr int PC_MIN_UNITS = 3;                  // fewer clusters rather than shorter ranges: every piece is
                                                  // one more to merge
 constexpr int PC_PLAN_KEPT = 1024;               // sequences, and query tiles, that the plan keeps in shared memory
-constexpr int PC_OVER = 3;                       // cost of a piece beyond its tiles, in tiles: a piece of n tiles
-                                                 // takes 5.2 + 1.65 n us
+constexpr int PC_OVER = 4;                       // cost of a piece beyond its tiles, in tiles: a piece of n tiles
+                                                 // takes about 5.2 + 1.65 n us (4 prompts of 611 .. 1733 tokens:
+                                                 // 255 us with 2, 246 with 3, 241 with 4 and 5)
 
 // A query tile: tokens t0 .. t0 + live - 1 of sequence b; token t attends
 // row_base + t rows (within the table).  The work of all query tiles is laid
