@@ -363,12 +363,26 @@ def _same_device(first, names, *others):
     return dev
 
 
-def _kept(t, stream):
-    """t, allocated here for use on `stream`: its memory is not handed out
-    again while that stream still uses it."""
+def _new(shape, dtype, dev, stream):
+    """A result that kernels on `stream` (None: the current stream) write.
+
+    It comes from that stream's own memory: a block of the current stream's
+    may still be in use by work queued there, which nothing orders before
+    `stream`.  The caller may go on with it on the current stream, so its
+    memory is not handed out again before what is queued there when it is
+    freed."""
+    t = _scratch(shape, dev, stream, dtype)
     if stream is not None:
-        t.record_stream(stream)
+        t.record_stream(torch.cuda.current_stream(dev))
     return t
+
+
+def _scratch(shape, dev, stream, dtype=torch.uint8):
+    """The same for what the kernels on `stream` alone use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _on(dev, stream, fn, *args):
@@ -415,7 +429,7 @@ def lca_page_tables(ctx_lens, new_lens, free_pages, taken, block_table, page_siz
 
     def made(t, name, dtype, size):
         if t is None:
-            return _kept(torch.empty(size, dtype=dtype, device=dev), stream)
+            return _new(size, dtype, dev, stream)
         _need(t, name, dtype, (size,))
         return t
 
@@ -473,10 +487,13 @@ def lca_append_paged(pages, rows, slot_map, stream=None):
         check(rc, "lca_append_paged")
 
 
+def _paged_bytes(B, T, max_new):
+    return max(int(_lib.lib().mla_paged_workspace_bytes(B, T, max_new)), 256)
+
+
 def paged_workspace(B: int, T: int, max_new: int, device=None) -> torch.Tensor:
     """Scratch for mla_paged_attn on a batch of B sequences and T tokens."""
-    n = int(_lib.lib().mla_paged_workspace_bytes(B, T, max_new))
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(_paged_bytes(B, T, max_new), dtype=torch.uint8, device=device or "cuda")
 
 
 def mla_paged_attn(pages, block_table, seq_lens, q_start, q, w_uv, max_new, scale=None, out=None, ws=None,
@@ -500,11 +517,11 @@ def mla_paged_attn(pages, block_table, seq_lens, q_start, q, w_uv, max_new, scal
     T = q.shape[0]
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
     if out is None:
-        out = _kept(torch.empty(T, H, D_V, dtype=torch.bfloat16, device=q.device), stream)
+        out = _new((T, H, D_V), torch.bfloat16, q.device, stream)
     else:
         _need(out, "out", torch.bfloat16, (T, H, D_V))
     if ws is None:
-        ws = _kept(paged_workspace(B, T, max_new, device=q.device), stream)
+        ws = _scratch(_paged_bytes(B, T, max_new), q.device, stream)
     dev = _same_device(pages, "block_table seq_lens q_start q w_uv out ws", block_table, seq_lens, q_start, q, w_uv,
                        out, ws)
     rc = _on(dev, stream, _lib.lib().mla_paged_attn, pages.data_ptr(), *pages.shape[:2], block_table.data_ptr(),

@@ -1,0 +1,86 @@
+"""Results and scratch that a call makes itself for a stream given to it: they
+never lie in memory that work queued on the current stream still uses."""
+import pytest
+import torch
+
+import mla_latent_space_lca_b200 as lca
+
+import paged_ref as ref
+from test_gpu_paged import DEV, SCALE, make, status_ok
+
+pytestmark = pytest.mark.gpu
+DELAY = 100_000_000   # clock cycles, 50 ms and more
+
+
+class Pending:
+    """Blocks of the given sizes that are free again for the current stream's
+    next allocation while that stream has yet to read and write them."""
+
+    def __init__(self, sizes):
+        blocks = [torch.empty(n, dtype=torch.uint8, device=DEV).fill_(5) for n in sizes]
+        self.kept = [torch.zeros(n, dtype=torch.uint8, device=DEV) for n in sizes]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(DELAY)
+        for b, k in zip(blocks, self.kept):
+            k.copy_(b)
+            b.fill_(255)
+
+    def check(self):
+        torch.cuda.synchronize()
+        assert all((k == 5).all() for k in self.kept)
+
+
+def nbytes(t):
+    return t.numel() * t.element_size()
+
+
+@pytest.mark.parametrize("lens,new,max_new", [([900, 4000, 70], [1, 1, 1], 1), ([900, 4000, 70], [40, 3, 1], 40)])
+def test_attention_on_a_stream_given(lens, new, max_new):
+    args = make(lens, new, 32, seed=max_new)
+    T = args[4].shape[0]
+    want = ref.attention(*args, SCALE)
+    s2 = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pending = Pending([nbytes(lca.paged_workspace(3, T, max_new)), T * 16 * 128 * 2])
+    out = lca.mla_paged_attn(*args, max_new, stream=s2)
+    pending.check()
+    status_ok()
+    ref.assert_attention(out, want)
+
+
+def test_tables_on_a_stream_given():
+    B, T, page = 700, 5000, 16
+    ctx = torch.arange(B, dtype=torch.int32, device=DEV) % 50
+    new = torch.full((B,), 7, dtype=torch.int32, device=DEV)
+    free = torch.arange(3000, dtype=torch.int32, device=DEV)
+    taken = torch.zeros(1, dtype=torch.int32, device=DEV)
+    table = torch.arange(B * 4, dtype=torch.int32, device=DEV).view(B, 4) + 5000
+    want = ref.tables(ctx.tolist(), new.tolist(), free.tolist(), 0, table.tolist(), page, T)
+    s2 = torch.cuda.Stream()
+    pending = Pending([4 * B, 4 * (B + 1), 8 * T, 4 * T, 4, 16])
+    got = lca.lca_page_tables(ctx, new, free, taken, table, page, T, stream=s2)
+    pending.check()
+    for g, w in zip(got, want):
+        assert g.tolist() == (w if isinstance(w, list) else [w])
+    assert table.tolist() == want[6]
+
+
+def test_a_result_still_read_by_the_current_stream():
+    # a result freed here while the current stream has yet to read it: the
+    # next call on the other stream must not get its memory
+    args = make([300, 90], [3, 2], 16, seed=1)
+    other = make([300, 90], [3, 2], 16, seed=2)
+    want = ref.attention(*args, SCALE)
+    s2 = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = lca.mla_paged_attn(*args, 3, stream=s2)
+    kept = torch.zeros_like(out)
+    torch.cuda.current_stream().wait_stream(s2)
+    torch.cuda._sleep(DELAY)
+    kept.copy_(out)
+    del out
+    again = lca.mla_paged_attn(*other, 3, stream=s2)
+    torch.cuda.synchronize()
+    status_ok()
+    ref.assert_attention(kept, want)
+    ref.assert_attention(again, ref.attention(*other, SCALE))
