@@ -37,6 +37,28 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _new(shape, dtype, dev, stream):
+    """A result that kernels on `stream` (None: the current stream) write.
+
+    It comes from that stream's own memory: a block of the current stream's
+    may still be in use by work queued there, which nothing orders before
+    `stream`.  The caller may go on with it on the current stream, so its
+    memory is not handed out again before what is queued there when it is
+    freed."""
+    t = _scratch(shape, dev, stream, dtype)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _scratch(shape, dev, stream, dtype=torch.uint8):
+    """The same for what the kernels on `stream` alone read and write."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _need(t, name, dtype, shape=None, host=False):
     """A contiguous tensor of this dtype (and shape) on the GPU, or, with
     host=True, in pinned host memory (read or written in place by the
@@ -84,10 +106,13 @@ def workspace_bytes(op: int, B: int, L: int, q_len: int = 0, g: int = 16, w: int
     return int(_lib.lib().lca_workspace_bytes(op, B, L, q_len, _params(g, w, None)))
 
 
+def _scratch_bytes(*args, **kw):
+    return max(workspace_bytes(*args, **kw), 256)
+
+
 def workspace(op: int, B: int, L: int, q_len: int = 0, g: int = 16, w: int = 1024,
               device=None) -> torch.Tensor:
-    n = workspace_bytes(op, B, L, q_len, g, w)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(_scratch_bytes(op, B, L, q_len, g, w), dtype=torch.uint8, device=device or "cuda")
 
 
 def mla_decode_attn(cache, q, w_uv, scale=None, out=None, o_lat=None, ws=None, stream=None):
@@ -95,11 +120,11 @@ def mla_decode_attn(cache, q, w_uv, scale=None, out=None, o_lat=None, ws=None, s
     pitch = _cache(cache)
     _need(q, "q", torch.bfloat16, (B, H, D))
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
-    out = torch.empty(B, H, D_V, dtype=torch.float32, device=cache.device) if out is None else out
+    out = _new((B, H, D_V), torch.float32, cache.device, stream) if out is None else out
     _need(out, "out", torch.float32, (B, H, D_V), host=True)
     if o_lat is not None:
         _need(o_lat, "o_lat", torch.float32, (B, H, D_C))
-    ws = workspace(_lib.OP_MLA_DECODE, B, L, device=cache.device) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_MLA_DECODE, B, L), cache.device, stream) if ws is None else ws
     if pitch:   # a strided cache: MLA decode through lca_decode with g = 1
         rc = _lib.lib().lca_decode(_ptr(cache), None, _ptr(q), _ptr(w_uv), B, L, _params(1, 0, scale, 0, pitch),
                                    _ptr(out), _ptr(o_lat), None, _ptr(ws), ws.numel(), _stream(stream))
@@ -119,8 +144,8 @@ def lca_condense(cache, q_recent, g=16, w=1024, scale=None, rep=None, anchor=Non
     _need(q_recent, "q_recent", torch.bfloat16, (B, g, H, D))
     m = num_groups(L, g, w)
     dev = cache.device
-    rep = torch.empty(B, m, D, dtype=torch.bfloat16, device=dev) if rep is None else rep
-    ws = workspace(_lib.OP_CONDENSE, B, L, g=g, w=w, device=dev) if ws is None else ws
+    rep = _new((B, m, D), torch.bfloat16, dev, stream) if rep is None else rep
+    ws = _scratch(_scratch_bytes(_lib.OP_CONDENSE, B, L, g=g, w=w), dev, stream) if ws is None else ws
     rc = _lib.lib().lca_condense(_ptr(cache), _ptr(q_recent), B, L, _params(g, w, scale, variant, pitch),
                                  _ptr(rep) if m > 0 else None, _ptr(anchor), _ptr(alpha), _ptr(ws),
                                  ws.numel(), _stream(stream))
@@ -137,11 +162,11 @@ def lca_decode_attn(cache, rep, q, w_uv, g=16, w=1024, scale=None, out=None, o_l
     m = num_groups(L, g, w)
     if m > 0:
         _need(rep, "rep", torch.bfloat16, (B, m, D))
-    out = torch.empty(B, H, D_V, dtype=torch.float32, device=cache.device) if out is None else out
+    out = _new((B, H, D_V), torch.float32, cache.device, stream) if out is None else out
     _need(out, "out", torch.float32, (B, H, D_V), host=True)
     if o_lat is not None:
         _need(o_lat, "o_lat", torch.float32, (B, H, D_C))
-    ws = workspace(_lib.OP_DECODE_ATTN, B, L, g=g, w=w, device=cache.device) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_DECODE_ATTN, B, L, g=g, w=w), cache.device, stream) if ws is None else ws
     rc = _lib.lib().lca_decode_attn(_ptr(cache), _ptr(rep) if m > 0 else None, _ptr(q), _ptr(w_uv),
                                     B, L, _params(g, w, scale, 0, pitch), _ptr(out), _ptr(o_lat), _ptr(ws),
                                     ws.numel(), _stream(stream))
@@ -160,7 +185,7 @@ def lca_condense_append(cache, q_recent, rep, j0, g=16, w=1024, scale=None, anch
     if rep.dim() != 3 or rep.shape[0] != B or rep.shape[2] != D:
         raise ValueError(f"rep has shape {tuple(rep.shape)}, expected ({B}, rep_cap, {D})")
     m = num_groups(L, g, w)
-    ws = workspace(_lib.OP_CONDENSE, B, L, g=g, w=w, device=cache.device) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_CONDENSE, B, L, g=g, w=w), cache.device, stream) if ws is None else ws
     rc = _lib.lib().lca_condense_append(_ptr(cache), _ptr(q_recent), B, L, _params(g, w, scale, variant, pitch), int(j0),
                                         _ptr(rep), rep.shape[1], _ptr(anchor), _ptr(alpha), _ptr(ws),
                                         ws.numel(), _stream(stream))
@@ -177,11 +202,11 @@ def lca_decode_stored(cache, rep, q, w_uv, g=16, w=1024, scale=None, out=None, o
     _need(q, "q", torch.bfloat16, (B, H, D))
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
     _need(rep, "rep", torch.bfloat16)
-    out = torch.empty(B, H, D_V, dtype=torch.float32, device=cache.device) if out is None else out
+    out = _new((B, H, D_V), torch.float32, cache.device, stream) if out is None else out
     _need(out, "out", torch.float32, (B, H, D_V), host=True)
     if o_lat is not None:
         _need(o_lat, "o_lat", torch.float32, (B, H, D_C))
-    ws = workspace(_lib.OP_DECODE_ATTN, B, L, g=g, w=w, device=cache.device) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_DECODE_ATTN, B, L, g=g, w=w), cache.device, stream) if ws is None else ws
     rc = _lib.lib().lca_decode_stored(_ptr(cache), _ptr(rep), rep.shape[1], _ptr(q), _ptr(w_uv), B, L,
                                       _params(g, w, scale, 0, pitch), _ptr(out), _ptr(o_lat), _ptr(ws), ws.numel(),
                                       _stream(stream))
@@ -197,11 +222,11 @@ def lca_decode(cache, q_recent, q, w_uv, g=16, w=1024, scale=None, out=None, o_l
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
     if g != 1:
         _need(q_recent, "q_recent", torch.bfloat16, (B, g, H, D))
-    out = torch.empty(B, H, D_V, dtype=torch.float32, device=cache.device) if out is None else out
+    out = _new((B, H, D_V), torch.float32, cache.device, stream) if out is None else out
     _need(out, "out", torch.float32, (B, H, D_V), host=True)
     if o_lat is not None:
         _need(o_lat, "o_lat", torch.float32, (B, H, D_C))
-    ws = workspace(_lib.OP_DECODE, B, L, g=g, w=w, device=cache.device) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_DECODE, B, L, g=g, w=w), cache.device, stream) if ws is None else ws
     rc = _lib.lib().lca_decode(_ptr(cache), _ptr(q_recent), _ptr(q), _ptr(w_uv), B, L,
                                _params(g, w, scale, 0, pitch), _ptr(out), _ptr(o_lat), _ptr(anchor), _ptr(ws),
                                ws.numel(), _stream(stream))
@@ -221,11 +246,11 @@ def lca_decode_varlen(cache, lens, q_recent, q, w_uv, g=16, w=1024, scale=None, 
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
     if g != 1:
         _need(q_recent, "q_recent", torch.bfloat16, (B, g, H, D))
-    out = torch.empty(B, H, D_V, dtype=torch.float32, device=cache.device) if out is None else out
+    out = _new((B, H, D_V), torch.float32, cache.device, stream) if out is None else out
     _need(out, "out", torch.float32, (B, H, D_V), host=True)
     if o_lat is not None:
         _need(o_lat, "o_lat", torch.float32, (B, H, D_C))
-    ws = workspace(_lib.OP_DECODE, B, L, g=g, w=w, device=cache.device) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_DECODE, B, L, g=g, w=w), cache.device, stream) if ws is None else ws
     rc = _lib.lib().lca_decode_varlen(_ptr(cache), _ptr(lens), _ptr(q_recent), _ptr(q), _ptr(w_uv), B, L,
                                       _params(g, w, scale, 0, pitch), _ptr(out), _ptr(o_lat), _ptr(anchor),
                                       _ptr(ws), ws.numel(), _stream(stream))
@@ -244,11 +269,11 @@ def lca_decode_stored_varlen(cache, rep, lens, q, w_uv, g=16, w=1024, scale=None
     _need(q, "q", torch.bfloat16, (B, H, D))
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
     _need(rep, "rep", torch.bfloat16)
-    out = torch.empty(B, H, D_V, dtype=torch.float32, device=cache.device) if out is None else out
+    out = _new((B, H, D_V), torch.float32, cache.device, stream) if out is None else out
     _need(out, "out", torch.float32, (B, H, D_V), host=True)
     if o_lat is not None:
         _need(o_lat, "o_lat", torch.float32, (B, H, D_C))
-    ws = workspace(_lib.OP_DECODE_ATTN, B, L, g=g, w=w, device=cache.device) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_DECODE_ATTN, B, L, g=g, w=w), cache.device, stream) if ws is None else ws
     rc = _lib.lib().lca_decode_stored_varlen(_ptr(cache), _ptr(rep), rep.shape[1], _ptr(lens), _ptr(q),
                                              _ptr(w_uv), B, L, _params(g, w, scale, 0, pitch), _ptr(out),
                                              _ptr(o_lat), _ptr(ws), ws.numel(), _stream(stream))
@@ -272,11 +297,11 @@ def lca_decode_shard(cache_shard, q_recent, q, L, row0, g=16, w=1024, scale=None
     if q_recent is not None:
         _need(q_recent, "q_recent", torch.bfloat16, (B, g, H, D))
     dev = cache_shard.device
-    part = torch.empty(shard_record_floats(B), dtype=torch.float32, device=dev) if part is None else part
+    part = _new(shard_record_floats(B), torch.float32, dev, stream) if part is None else part
     _need(part, "part", torch.float32, (shard_record_floats(B),))
     if anchor is not None:
         _need(anchor, "anchor", torch.int32)
-    ws = workspace(_lib.OP_DECODE, B, L, g=g, w=w, device=dev) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_DECODE, B, L, g=g, w=w), dev, stream) if ws is None else ws
     rc = _lib.lib().lca_decode_shard(_ptr(cache_shard), _ptr(q_recent), _ptr(q), B, L, row0, Ls,
                                      _params(g, w, scale, 0, pitch), _ptr(part), _ptr(anchor), _ptr(ws),
                                      ws.numel(), _stream(stream))
@@ -289,7 +314,7 @@ def lca_combine_shards(parts, w_uv, B, out=None, o_lat=None, stream=None):
     n = parts.shape[0]
     _need(parts, "parts", torch.float32, (n, shard_record_floats(B)))
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
-    out = torch.empty(B, H, D_V, dtype=torch.float32, device=parts.device) if out is None else out
+    out = _new((B, H, D_V), torch.float32, parts.device, stream) if out is None else out
     _need(out, "out", torch.float32, (B, H, D_V), host=True)
     if o_lat is not None:
         _need(o_lat, "o_lat", torch.float32, (B, H, D_C))
@@ -305,14 +330,13 @@ def lca_prefill_block(cache, q, w_uv, q_start, q_len, g=16, w=1024, scale=None, 
     pitch = _cache(cache)
     _need(q, "q", torch.bfloat16, (B, L, H, D))
     _need(w_uv, "w_uv", torch.bfloat16, (H, D_C, D_V))
-    out = (torch.empty(B, q_len, H, D_V, dtype=torch.float32, device=cache.device)
-           if out is None else out)
+    out = _new((B, q_len, H, D_V), torch.float32, cache.device, stream) if out is None else out
     _need(out, "out", torch.float32, (B, q_len, H, D_V), host=True)
     if o_lat is not None:
         _need(o_lat, "o_lat", torch.float32, (B, q_len, H, D_C))
     if anchor is not None:
         _need(anchor, "anchor", torch.int32)
-    ws = workspace(_lib.OP_PREFILL, B, L, q_len, g=g, w=w, device=cache.device) if ws is None else ws
+    ws = _scratch(_scratch_bytes(_lib.OP_PREFILL, B, L, q_len, g=g, w=w), cache.device, stream) if ws is None else ws
     rc = _lib.lib().lca_prefill_block(_ptr(cache), _ptr(q), _ptr(w_uv), B, L, q_start, q_len,
                                       _params(g, w, scale, variant, pitch), _ptr(out), _ptr(o_lat), _ptr(anchor),
                                       _ptr(ws), ws.numel(), _stream(stream))
@@ -361,28 +385,6 @@ def _same_device(first, names, *others):
             bad = next(n for n, o in zip(names.split(), others) if o is t)
             raise ValueError(f"{bad} is on {t.device}, expected {first.device}")
     return dev
-
-
-def _new(shape, dtype, dev, stream):
-    """A result that kernels on `stream` (None: the current stream) write.
-
-    It comes from that stream's own memory: a block of the current stream's
-    may still be in use by work queued there, which nothing orders before
-    `stream`.  The caller may go on with it on the current stream, so its
-    memory is not handed out again before what is queued there when it is
-    freed."""
-    t = _scratch(shape, dev, stream, dtype)
-    if stream is not None:
-        t.record_stream(torch.cuda.current_stream(dev))
-    return t
-
-
-def _scratch(shape, dev, stream, dtype=torch.uint8):
-    """The same for what the kernels on `stream` alone use."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _on(dev, stream, fn, *args):

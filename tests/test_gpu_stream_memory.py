@@ -84,3 +84,49 @@ def test_a_result_still_read_by_the_current_stream():
     status_ok()
     ref.assert_attention(kept, want)
     ref.assert_attention(again, ref.attention(*other, SCALE))
+
+
+def decode_inputs(B=3, L=5000, seed=4):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *shape: torch.randn(*shape, generator=g, device=DEV).to(torch.bfloat16)  # noqa: E731
+    return {"cache": r(B, L, 576), "ring": r(B, 16, 16, 576), "q": r(B, 16, 576),
+            "w_uv": (r(16, 512, 128).float() / 512 ** 0.5).to(torch.bfloat16),
+            "lens": torch.tensor([L, 70, L - 1300][:B], dtype=torch.int32, device=DEV)}
+
+
+CONTIGUOUS = {
+    "mla_decode_attn": lambda s, **k: lca.mla_decode_attn(s["cache"], s["q"], s["w_uv"], **k),
+    "lca_condense": lambda s, **k: lca.lca_condense(s["cache"], s["ring"], **k),
+    "lca_decode_attn": lambda s, **k: lca.lca_decode_attn(s["cache"], s["rep"], s["q"], s["w_uv"], **k),
+    "lca_decode_stored": lambda s, **k: lca.lca_decode_stored(s["cache"], s["rep"], s["q"], s["w_uv"], **k),
+    "lca_decode": lambda s, **k: lca.lca_decode(s["cache"], s["ring"], s["q"], s["w_uv"], **k),
+    "lca_decode_varlen": lambda s, **k: lca.lca_decode_varlen(s["cache"], s["lens"], s["ring"], s["q"], s["w_uv"], **k),
+    "lca_decode_stored_varlen": lambda s, **k: lca.lca_decode_stored_varlen(s["cache"], s["rep"], s["lens"], s["q"],
+                                                                            s["w_uv"], **k),
+    "lca_decode_shard": lambda s, **k: lca.lca_decode_shard(s["cache"], s["ring"], s["q"], 5000, 0, **k),
+    "lca_combine_shards": lambda s, **k: lca.lca_combine_shards(s["parts"], s["w_uv"], 3, **k),
+    "lca_prefill_block": lambda s, **k: lca.lca_prefill_block(s["cache"][:1], s["q_all"], s["w_uv"], 1200, 64, **k),
+}
+OPS = {"mla_decode_attn": 0, "lca_condense": 1, "lca_decode_attn": 2, "lca_decode_stored": 2, "lca_decode": 3,
+       "lca_decode_varlen": 3, "lca_decode_stored_varlen": 2, "lca_decode_shard": 3, "lca_prefill_block": 4}
+
+
+@pytest.mark.parametrize("name", list(CONTIGUOUS))
+def test_contiguous_calls_on_a_stream_given(name):
+    s = decode_inputs()
+    s["rep"] = lca.lca_condense(s["cache"], s["ring"])
+    s["parts"] = lca.lca_decode_shard(s["cache"], s["ring"], s["q"], 5000, 0)[None]
+    s["q_all"] = torch.randn(1, 5000, 16, 576, device=DEV).to(torch.bfloat16)
+    call = CONTIGUOUS[name]
+    want = call(s)
+    sizes = [nbytes(want)]
+    if name in OPS:
+        B, q_len = (1, 64) if name == "lca_prefill_block" else (3, 0)
+        sizes.append(nbytes(lca.workspace(OPS[name], B, 5000, q_len)))
+    s2 = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pending = Pending(sizes)
+    got = call(s, stream=s2)
+    pending.check()
+    status_ok()
+    assert torch.equal(got, want)
