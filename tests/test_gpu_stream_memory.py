@@ -49,7 +49,7 @@ def test_attention_on_a_stream_given(lens, new, max_new):
 
 
 def test_tables_on_a_stream_given():
-    B, T, page = 700, 5000, 16
+    B, T, page = 700, 400_000, 16   # (above 1 MB the freed blocks are sure to be the next ones handed out)
     ctx = torch.arange(B, dtype=torch.int32, device=DEV) % 50
     new = torch.full((B,), 7, dtype=torch.int32, device=DEV)
     free = torch.arange(3000, dtype=torch.int32, device=DEV)
