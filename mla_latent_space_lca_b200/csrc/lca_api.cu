@@ -446,7 +446,7 @@ int run_attention(DeviceInfo *dev, const void *cache, const void *rep, const voi
         Launch l(st, K_COMBINE);
         // rows per CTA: enough CTAs (16 heads x row groups) to cover the SMs
         const int rpc = std::max(1, std::min(TD_ROWS, (LCA_HEADS * B + dev->sms - 1) / dev->sms));
-        const cudaError_t e = launch_ex(tail_decode_kernel<>, dim3(LCA_HEADS, (B + rpc - 1) / rpc), dim3(256),
+        const cudaError_t e = launch_ex(tail_decode_kernel<>, tail_grid(B, rpc), dim3(256),
                                         TD_SMEM_ALLOC, st, true, map_w, (const float *)w.part_o,
                                         (const float *)w.part_ml, B, a.n_tiles, a.T, a.G, o_lat, out, rpc,
                                         lse_out, 0, int64_t(0), (const int32_t *)a.tile_start,
@@ -601,7 +601,7 @@ int run_paged_tokens(DeviceInfo *dev, const PagedCall &c, const PagedWs &w)
     }
     Launch l(c.st, K_COMBINE);
     const int rpc = int(std::max<int64_t>(1, std::min<int64_t>(TD_ROWS, (LCA_HEADS * c.T + dev->sms - 1) / dev->sms)));
-    const cudaError_t e = launch_ex(tail_decode_kernel<true>, dim3(LCA_HEADS, (T + rpc - 1) / rpc), dim3(256),
+    const cudaError_t e = launch_ex(tail_decode_kernel<true>, tail_grid(T, rpc), dim3(256),
                                     TD_SMEM_ALLOC, c.st, true, map_w, (const float *)w.part_o,
                                     (const float *)w.part_ml, T, 0, int64_t(0), a.G, (float *)nullptr,
                                     (float *)nullptr, rpc, (float *)nullptr, 0, int64_t(0),
@@ -1002,7 +1002,7 @@ int lca_combine_shards(const float *parts, int n_shards, int B, const void *w_uv
     Launch l(st, K_COMBINE);
     const int rpc = std::max(1, std::min(TD_ROWS, (LCA_HEADS * B + dev->sms - 1) / dev->sms));
     const int64_t stride = int64_t(B) * LCA_HEADS * LCA_SHARD_RECORD_PER_HEAD;
-    const cudaError_t e = launch_ex(tail_decode_kernel<>, dim3(LCA_HEADS, (B + rpc - 1) / rpc), dim3(256),
+    const cudaError_t e = launch_ex(tail_decode_kernel<>, tail_grid(B, rpc), dim3(256),
                                     TD_SMEM_ALLOC, st, false, map_w, parts, (const float *)nullptr, B, 0,
                                     int64_t(0), 0, o_lat, out, rpc, (float *)nullptr, n_shards, stride,
                                     (const int32_t *)nullptr, (uint16_t *)nullptr, (const int32_t *)nullptr);

@@ -127,9 +127,10 @@ __global__ void __launch_bounds__(128, 1)
 // per-head W_UV up-projection, swap-AB so the tensor-core M dimension is the
 // 128 output columns:
 //   out^T[128 x 16] = W_UV[h]^T[128 x 512] * o^T[512 x 16]
-// (N = 16: up to 8 batch rows per CTA, the rest zero).  Grid (16 heads,
-// ceil(B/rpc)), 256 threads, rpc rows per CTA chosen by the host so that the
-// grid fills the GPU (fewer rows per CTA = more warps per row's slots).  W_UV[h] (128 KB, MN-major A) is TMA-loaded before
+// (N = 16: up to 8 batch rows per CTA, the rest zero).  Grid 16 heads x
+// ceil(B/rpc) row groups (tail_grid), 256 threads, rpc rows per CTA chosen by
+// the host so that the grid fills the GPU (fewer rows per CTA = more warps per
+// row's slots).  W_UV[h] (128 KB, MN-major A) is TMA-loaded before
 // waiting on the attention kernel.  Combine: with nb rows, each row gets
 // 8/nb warps (at least one); a warp merges its share of the row's partial
 // slots online (rescaling on a new maximum, lanes own 16 of the 512 columns),
@@ -166,6 +167,10 @@ constexpr int TD_OFF_BAR = TD_OFF_COEF + TD_ROWS * 8 * 4;
 constexpr int TD_SMEM = TD_OFF_BAR + 256;
 constexpr int TD_SMEM_ALLOC = TD_SMEM + 1024;
 
+// The heads of one row group after another, in x: y ends at 65535, which a
+// batch of single tokens can pass.
+inline dim3 tail_grid(int rows, int rpc) { return dim3(LCA_HEADS * unsigned((rows + rpc - 1) / rpc)); }
+
 template <bool PAGED = false>
 __global__ void __launch_bounds__(256, 1)
     tail_decode_kernel(const __grid_constant__ CUtensorMap map_w, const float *__restrict__ part_o,
@@ -180,8 +185,8 @@ __global__ void __launch_bounds__(256, 1)
         (reinterpret_cast<uintptr_t>(td_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x;
-    const int b0 = blockIdx.y * rpc;           // rpc <= TD_ROWS rows (sequences) per CTA
+    const int h = blockIdx.x % LCA_HEADS;
+    const int b0 = int(blockIdx.x / LCA_HEADS) * rpc;   // rpc <= TD_ROWS rows (sequences) per CTA
     const int nb = min(rpc, B - b0);
     const int wpr = max(1, TD_ROWS / nb);     // warps per row
     const bool gemm = PAGED || out != nullptr;
