@@ -483,6 +483,8 @@ def lca_append_paged(pages, rows, slot_map, stream=None):
         usual = False
     if not usual:
         dev, n_pages, page, T, pitch = _append_args(pages, rows, slot_map)
+    elif T <= 1:
+        pitch = D   # a row alone has none
     rc = _on(dev, stream, _lib.lib().lca_append_paged, rows.data_ptr(), pitch, slot_map.data_ptr(), T, pages.data_ptr(),
              n_pages, page)
     if rc:

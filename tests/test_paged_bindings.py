@@ -1,0 +1,41 @@
+"""What the bindings of the paged cache pass on to the library, and what they
+refuse, on the host (no GPU): tensors without memory on a CUDA device."""
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+import mla_latent_space_lca_b200 as lca
+from mla_latent_space_lca_b200 import api
+
+
+@pytest.fixture
+def calls(monkeypatch, lcalib):
+    """The arguments of every call that reaches the library."""
+    made = []
+
+    def on(dev, stream, fn, *args):
+        made.append(args)
+        return 0
+
+    monkeypatch.setattr(api, "_on", on)
+    with FakeTensorMode():
+        yield made
+
+
+def cuda(*shape, dtype=torch.bfloat16):
+    return torch.empty(*shape, dtype=dtype, device="cuda")
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+@pytest.mark.parametrize("width", [576, 577, 580, 584, 1000])
+@pytest.mark.parametrize("T", [0, 1])
+def test_append_of_one_row_whatever_its_stride(calls, T, width):
+    lca.lca_append_paged(cuda(4, 16, 576), cuda(T, width)[:, :576], cuda(T, dtype=torch.int64))
+    assert len(calls) == 1 and calls[0][1] % 8 == 0 and calls[0][3] == T
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_append_keeps_the_pitch_of_several_rows(calls):
+    lca.lca_append_paged(cuda(4, 16, 576), cuda(3, 640)[:, :576], cuda(3, dtype=torch.int64))
+    lca.lca_append_paged(cuda(4, 16, 576), cuda(3, 580)[:, :576], cuda(3, dtype=torch.int64))   # the library refuses it
+    assert [c[1] for c in calls] == [640, 580]
