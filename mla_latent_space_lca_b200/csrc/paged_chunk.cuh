@@ -487,6 +487,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
+// Power of two that brings a reference m of 2^30 and more below 2^30 (1 below
+// that).  A weight's exponent z - m is one multiply-add of the logit, so it holds
+// what m was rounded by, up to 2^-24 |m|: a factor that all of a row's weights
+// share, but none that fp32 holds where m reaches 2^31 (the weights were all
+// infinite or zero there).  Shrunk, it is 2^32 at most, and logits that differ in
+// fp32 are still 2^5 or more apart: the weights stay one-hot.
+__device__ __forceinline__ float shrink_of(float m)
+{
+    const uint32_t e = __float_as_uint(m) & 0x7f800000u;
+    return __uint_as_float(min((283u << 23) - e, 127u << 23));
+}
+
 // A cluster's pieces: query tile q and the cache tiles [k0, k1) of it.
 struct ChunkPiece {
     ChunkTile t;
@@ -956,7 +968,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     m = tmax;
                     l *= f;
                 }
-                const uint64_t scale = pack2(a.sl2, a.sl2), shift = pack2(-m, -m);
+                const float shrink = shrink_of(m), mul = a.sl2 * shrink, off = m * -shrink;
+                const uint64_t scale = pack2(mul, mul), shift = pack2(off, off);
                 uint64_t sum[2] = {0, 0};
                 uint32_t pk[32];
 #pragma unroll
