@@ -131,6 +131,10 @@ struct AttnArgs {
 };
 constexpr int AT_PLAN_ITEMS = 128;
 
+// The maximum of no logits at all (every page missing): finite, so that
+// -infinity minus it is -infinity, and below every logit that is finite.
+constexpr float NO_ROW = -3.402823466e38f;
+
 // Shared-memory layout of a 64-row tile.  A contiguous cache's tile arrives as
 // nine [64 rows x 64 columns] blocks.  A paged cache's tile arrives page by
 // page, as [8 groups of 8 rows][9 chunks of 64 columns][8 rows x 128 B]: the
@@ -913,7 +917,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
                     }
                     tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
                     tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
-                    if constexpr (PAGED) tmax = fmaxf(tmax, -1e30f);   // a tile without any page
+                    if constexpr (PAGED) tmax = fmaxf(tmax, NO_ROW);   // a tile without any page
                     if (i == first) {
                         m_use = tmax;
                     } else if (tmax > m_use + 8.f) {

@@ -879,7 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
             // rows that every live token of the tile (of both CTAs) attends
             const int32_t nv_all = clamp_rows(w.t.row_base + w.t.t0, max_rows);
             const int nvs_last = tiles ? w.v_slots(tiles - 1, max_rows) : 0;
-            float m = -1e30f, l = 0.f;
+            float m = NO_ROW, l = 0.f;
             int32_t row0 = w.k0 * PC_TILE;
             // lane c looks up the c-th of a tile's pages, a tile ahead
             const int32_t *table = a.block_table + size_t(w.t.b) * size_t(a.max_blocks);
@@ -962,7 +962,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                 tmax = fmaxf(tmax, exchange(tmax)) * a.sl2;
                 float f = 1.f;
                 if (i == 0) {
-                    m = fmaxf(tmax, -1e30f);
+                    m = fmaxf(tmax, NO_ROW);
                 } else if (tmax > m + 8.f) {
                     f = fast_exp2(m - tmax);
                     m = tmax;
@@ -1122,13 +1122,13 @@ __global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs
     const ChunkMerge mg = p.merge[blockIdx.y + 1];
     if (mg.c1 < 0 || r / LCA_HEADS >= mg.live) return;
     const auto slot = [&](int k) { return size_t(k == mg.c0 ? 2 * k + 1 : 2 * k) * PC_ROWS + r; };
-    float M = -1e30f, den = 0.f, acc[16];
+    float M = NO_ROW, den = 0.f, acc[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
     // 32 pieces at a time, a lane each: maximum, weight, sum; then all lanes the values
     for (int k0 = mg.c0; k0 <= mg.c1; k0 += 32) {
         const int k = k0 + lane;
-        float2 ml = make_float2(-1e30f, 0.f);
+        float2 ml = make_float2(NO_ROW, 0.f);
         if (k <= mg.c1) ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(k) * 2);
         float top = ml.x;
 #pragma unroll

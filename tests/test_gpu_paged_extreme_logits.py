@@ -63,3 +63,20 @@ def test_logits_that_differ_in_their_last_bits(steps, exponent, hint):
     q.zero_()
     q[:, :, 0] = 2.0 ** (exponent - exponent // 2 + 4)
     check(pages, table, lens, start, q, w_uv, hint)
+
+
+def ramp(lens, new, page, first, last, seed, size=1.0):
+    """Rows along one direction: logits from `first` to `last` by position."""
+    pages, table, lens, start, q, w_uv = make([lens], [new], page, seed=seed)
+    ids = table[0, : -(-int(lens[0]) // page)].long()
+    unit = q[0, 0].float() / q[0, 0].float().norm()
+    q[:] = (unit * size).to(torch.bfloat16)
+    z = torch.linspace(first, last, ids.numel() * page, dtype=torch.float64, device=DEV)
+    pages[ids] = (z.view(-1, page, 1) * unit.double() / (SCALE * size)).to(torch.bfloat16)
+    return pages, table, lens, start, q, w_uv
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("first,last", [(-3e33, -1e32), (-1e32, -3e33), (-1e25, -1e24), (3e35, -3e35), (-3e35, 3e35)])
+def test_logits_of_any_sign(first, last, hint):
+    check(*ramp(20, 5, 16, first, last, seed=2, size=1e15), hint)
