@@ -526,6 +526,8 @@ def mla_paged_attn(pages, block_table, seq_lens, q_start, q, w_uv, max_new, scal
         _need(out, "out", torch.bfloat16, (T, H, D_V))
     if ws is None:
         ws = _scratch(_paged_bytes(B, T, max_new), q.device, stream)
+    elif not ws.is_contiguous():   # its bytes are counted by its shape
+        raise ValueError("ws must be contiguous")
     dev = _same_device(pages, "block_table seq_lens q_start q w_uv out ws", block_table, seq_lens, q_start, q, w_uv,
                        out, ws)
     rc = _on(dev, stream, _lib.lib().mla_paged_attn, pages.data_ptr(), *pages.shape[:2], block_table.data_ptr(),

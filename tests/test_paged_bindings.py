@@ -39,3 +39,18 @@ def test_append_keeps_the_pitch_of_several_rows(calls):
     lca.lca_append_paged(cuda(4, 16, 576), cuda(3, 640)[:, :576], cuda(3, dtype=torch.int64))
     lca.lca_append_paged(cuda(4, 16, 576), cuda(3, 580)[:, :576], cuda(3, dtype=torch.int64))   # the library refuses it
     assert [c[1] for c in calls] == [640, 580]
+
+
+def attention_args(T=6, B=2):
+    i32 = lambda *shape: cuda(*shape, dtype=torch.int32)  # noqa: E731
+    return cuda(4, 16, 576), i32(B, 2), i32(B), i32(B + 1), cuda(T, 16, 576), cuda(16, 512, 128)
+
+
+def test_workspace_without_memory_of_its_own(calls):
+    # as many bytes as it needs by its shape, one by its memory
+    ws = cuda(1, dtype=torch.uint8).expand(1 << 30)
+    with pytest.raises(ValueError, match="ws"):
+        lca.mla_paged_attn(*attention_args(), 3, ws=ws)
+    with pytest.raises((TypeError, ValueError), match="ws"):
+        lca.mla_paged_attn(*attention_args(), 3, ws=torch.empty(1 << 30, dtype=torch.uint8))
+    assert not calls
