@@ -422,6 +422,8 @@ def lca_page_tables(ctx_lens, new_lens, free_pages, taken, block_table, page_siz
     B, dev, n = ctx_lens.shape[0], ctx_lens.device, int(max_tokens)
     if n < 0:
         raise ValueError("max_tokens must not be negative")
+    if not -2 ** 31 <= page_size < 2 ** 31:   # (the library refuses the others)
+        raise ValueError(f"page_size must be a power of two from 16 to 65536, got {page_size}")
     _need(new_lens, "new_lens", torch.int32, (B,))
     _need(free_pages, "free_pages", torch.int32)
     _need(taken, "taken", torch.int32, (1,))
@@ -491,8 +493,13 @@ def lca_append_paged(pages, rows, slot_map, stream=None):
         check(rc, "lca_append_paged")
 
 
+def _most_new(max_new):
+    """max_new as the library's int32: more than that is as good as that."""
+    return min(int(max_new), 2 ** 31 - 1)
+
+
 def _paged_bytes(B, T, max_new):
-    return max(int(_lib.lib().mla_paged_workspace_bytes(B, T, max_new)), 256)
+    return max(int(_lib.lib().mla_paged_workspace_bytes(B, T, _most_new(max_new))), 256)
 
 
 def paged_workspace(B: int, T: int, max_new: int, device=None) -> torch.Tensor:
@@ -532,7 +539,7 @@ def mla_paged_attn(pages, block_table, seq_lens, q_start, q, w_uv, max_new, scal
                        out, ws)
     rc = _on(dev, stream, _lib.lib().mla_paged_attn, pages.data_ptr(), *pages.shape[:2], block_table.data_ptr(),
              block_table.shape[1], seq_lens.data_ptr(), q_start.data_ptr(), q.data_ptr(), w_uv.data_ptr(), B, T,
-             int(max_new), float(default_scale() if scale is None else scale), out.data_ptr(), ws.data_ptr(),
+             _most_new(max_new), float(default_scale() if scale is None else scale), out.data_ptr(), ws.data_ptr(),
              ws.numel() * ws.element_size())
     if rc:
         check(rc, "mla_paged_attn")

@@ -54,3 +54,22 @@ def test_workspace_without_memory_of_its_own(calls):
     with pytest.raises((TypeError, ValueError), match="ws"):
         lca.mla_paged_attn(*attention_args(), 3, ws=torch.empty(1 << 30, dtype=torch.uint8))
     assert not calls
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+@pytest.mark.parametrize("max_new", [2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 40])
+def test_most_new_tokens_beyond_32_bits(calls, max_new):
+    # any number: 2^32 + 1 is not the single-token form's 1, nor 2^32 no number at all
+    lca.mla_paged_attn(*attention_args(), max_new)
+    (args,) = calls
+    assert args[10:12] == (6, 2 ** 31 - 1)   # T, max_new
+    assert lca.paged_workspace(2, 6, max_new).numel() == lca.paged_workspace(2, 6, 2).numel() == args[15]
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+@pytest.mark.parametrize("page_size", [2 ** 32 + 16, 2 ** 31, -2 ** 32 + 64])
+def test_page_size_beyond_32_bits(calls, page_size):
+    i32 = lambda *shape: cuda(*shape, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError, match="page_size"):
+        lca.lca_page_tables(i32(2), i32(2), i32(9), i32(1), i32(2, 4), page_size, 8)
+    assert not calls
