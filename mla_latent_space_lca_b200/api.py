@@ -112,7 +112,7 @@ def _scratch_bytes(*args, **kw):
 
 def workspace(op: int, B: int, L: int, q_len: int = 0, g: int = 16, w: int = 1024,
               device=None) -> torch.Tensor:
-    return torch.empty(_scratch_bytes(op, B, L, q_len, g, w), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(_scratch_bytes(op, B, L, q_len, g, w), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def mla_decode_attn(cache, q, w_uv, scale=None, out=None, o_lat=None, ws=None, stream=None):
@@ -504,7 +504,7 @@ def _paged_bytes(B, T, max_new):
 
 def paged_workspace(B: int, T: int, max_new: int, device=None) -> torch.Tensor:
     """Scratch for mla_paged_attn on a batch of B sequences and T tokens."""
-    return torch.empty(_paged_bytes(B, T, max_new), dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(_paged_bytes(B, T, max_new), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def mla_paged_attn(pages, block_table, seq_lens, q_start, q, w_uv, max_new, scale=None, out=None, ws=None,

@@ -73,3 +73,12 @@ def test_page_size_beyond_32_bits(calls, page_size):
     with pytest.raises(ValueError, match="page_size"):
         lca.lca_page_tables(i32(2), i32(2), i32(9), i32(1), i32(2, 4), page_size, 8)
     assert not calls
+
+
+def test_workspace_on_the_device_named(monkeypatch, lcalib):
+    asked = []
+    monkeypatch.setattr(api.torch, "empty", lambda *a, **kw: asked.append(kw["device"]))
+    lca.paged_workspace(1, 1, 1, device=0)   # whichever device is current
+    lca.workspace(3, 1, 2048, device=0)
+    lca.paged_workspace(1, 1, 1)
+    assert asked == [0, 0, "cuda"]
