@@ -405,7 +405,8 @@ int lca_append_paged(const void *rows, int64_t row_pitch, const int64_t *slot_ma
  *   out  [T][16][128] bf16; rows that belong to no sequence (from q_start[B]
  *        on, in a padded batch) are left as they were.
  * Pages may hold anything in rows that no token of the call attends, NaN and
- * infinities included.  max_new: the most new tokens any sequence may have, a
+ * infinities included; the result of a token is not defined where a row that it
+ * attends, or its query, holds them (it need not be NaN).  max_new: the most new tokens any sequence may have, a
  * hint that selects the kernel (1: single tokens); the result is right
  * whatever it says.  Logits, softmax and sums are fp32; the softmax weights enter the
  * value product as bf16.
@@ -413,7 +414,10 @@ int lca_append_paged(const void *rows, int64_t row_pitch, const int64_t *slot_ma
  * with max_new = 1, T * max_blocks * page_size / 64 < 2^30
  * (LCA_ERR_UNSUPPORTED otherwise).  T == 0 is valid.
  * ws: mla_paged_workspace_bytes(B, T, max_new), used by one call at a time: two
- * calls (or captured graphs) that may run at once need one each. */
+ * calls (or captured graphs) that may run at once need one each.  It grows with
+ * T, by 33 KB a token: 109 MB for 2048 new tokens, 1.1 GB for 32768.  A long
+ * prompt can be given in parts, one call after the other, each with its tokens
+ * and the length up to its last one. */
 size_t mla_paged_workspace_bytes(int B, int64_t T, int max_new);
 int mla_paged_attn(const void *pages, int64_t n_pages, int page_size, const int32_t *block_table, int64_t max_blocks,
                    const int32_t *seq_lens, const int32_t *q_start, const void *q, const void *w_uv, int B, int64_t T,

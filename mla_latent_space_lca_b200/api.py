@@ -503,7 +503,8 @@ def _paged_bytes(B, T, max_new):
 
 
 def paged_workspace(B: int, T: int, max_new: int, device=None) -> torch.Tensor:
-    """Scratch for mla_paged_attn on a batch of B sequences and T tokens."""
+    """Scratch for mla_paged_attn on a batch of B sequences and T tokens: 33 KB
+    a token, and 42 MB more where max_new is above 1."""
     return torch.empty(_paged_bytes(B, T, max_new), dtype=torch.uint8, device="cuda" if device is None else device)
 
 

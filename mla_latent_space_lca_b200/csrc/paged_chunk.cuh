@@ -78,9 +78,11 @@ constexpr int PC_MAX_CLUSTERS = 80;              // partial outputs: two per clu
 constexpr int PC_MIN_UNITS = 3;                  // fewer clusters rather than shorter ranges: every piece is
                                                  // one more to merge
 constexpr int PC_PLAN_KEPT = 1024;               // sequences, and query tiles, that the plan keeps in shared memory
-constexpr int PC_OVER = 4;                       // cost of a piece beyond its tiles, in tiles: a piece of n tiles
-                                                 // takes about 5.2 + 1.65 n us (4 prompts of 611 .. 1733 tokens:
-                                                 // 255 us with 2, 246 with 3, 241 with 4 and 5)
+constexpr int PC_OVER = 4;                       // cost of a piece beyond its tiles, in tiles.  A piece of n tiles
+                                                 // takes about 5.2 + 1.65 n us, which says 3.2; taken by
+                                                 // measurement instead: with 2, 3, 4, 5 four prompts of 611 ..
+                                                 // 1733 tokens take 255, 246, 241, 241 us, 16 x 2..5 tokens 65.3,
+                                                 // 65.8, 66.0, 66.3, a mixed batch 176.5, 176, 175, 175.5
 
 // A query tile: tokens t0 .. t0 + live - 1 of sequence b; token t attends
 // row_base + t rows (within the table).  The work of all query tiles is laid
@@ -908,7 +910,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PC_THREADS, 1)
                     // logit against it non-finite: look those rows up and
                     // clear what is not finite in this CTA's columns of them
                     // (a token that does attend the row has the NaN in its
-                    // weight already).
+                    // weight already, unless its logit is minus infinity,
+                    // which leaves the row out).
                     const int nvs = i + 1 == tiles ? nvs_last : PC_VS;
                     bool waited = false;
 #pragma unroll
@@ -1145,6 +1148,8 @@ __global__ void __launch_bounds__(MG_THREADS) paged_merge_kernel(const ChunkArgs
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[e] *= old;
         const int n = min(32, mg.c1 - k0 + 1);
+        // (four pieces' values asked for together; the build's 54 registers
+        // hold about half of them at a time)
         for (int i0 = 0; i0 < n; i0 += 4) {
             float fi[4];
             float4 x[4][4];
