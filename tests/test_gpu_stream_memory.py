@@ -130,3 +130,27 @@ def test_contiguous_calls_on_a_stream_given(name):
     pending.check()
     status_ok()
     assert torch.equal(got, want)
+
+
+def test_captured_on_a_stream_that_joins_the_capture():
+    args = make([900, 300, 64], [1, 7, 3], 32, seed=9)
+    s = decode_inputs()
+    want, plain = ref.attention(*args, SCALE), lca.lca_decode(s["cache"], s["ring"], s["q"], s["w_uv"])
+    lca.mla_paged_attn(*args, 7)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = lca.mla_paged_attn(*args, 7, stream=side)
+        again = lca.mla_paged_attn(*args, 1, stream=side)
+        fused = lca.lca_decode(s["cache"], s["ring"], s["q"], s["w_uv"], stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for t in (out, again, fused):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        status_ok()
+        ref.assert_attention(out, want)
+        ref.assert_attention(again, want)
+        assert torch.equal(fused, plain)
